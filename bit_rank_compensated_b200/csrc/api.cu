@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "host.h"
 #include "internal.h"
 #include "svdq.h"
 
@@ -20,13 +21,11 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
+struct DeviceSlot {
   std::once_flag once;
-  svdq_status arch = SVDQ_OK;
-  int num_sms = 0;
-  uint32_t *err = nullptr;
+  DeviceState state;
 };
-DeviceState g_dev[kMaxDevices];
+DeviceSlot g_dev[kMaxDevices];
 
 // Compute capability that svdq_test_override_capability asks device_check to assume
 // (major * 10 + minor), or -1. It can only make a supported GPU look unsupported.
@@ -61,14 +60,17 @@ struct HostPipe {
 };
 HostPipe g_pipe[kMaxDevices];
 
+}  // namespace
+
 svdq_status device_check(DeviceState **out) {
   const int ov = g_cap_override.load(std::memory_order_relaxed);
   if (ov >= 0 && ov != 100) return SVDQ_ERR_UNSUPPORTED_ARCH;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SVDQ_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return SVDQ_ERR_INTERNAL;
-  DeviceState &d = g_dev[dev];
-  std::call_once(d.once, [&]() {
+  DeviceState &d = g_dev[dev].state;
+  std::call_once(g_dev[dev].once, [&]() {
+    d.index = dev;
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
@@ -92,7 +94,7 @@ svdq_status device_check(DeviceState **out) {
   return SVDQ_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
@@ -116,6 +118,8 @@ svdq_status check_layer(const svdq_layer *L) {
   return SVDQ_OK;
 }
 
+}  // namespace
+
 bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
   std::call_once(g_encode_once, init_encode);
@@ -128,6 +132,8 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
 CUtensorMapSwizzle swizzle_for_row_bytes(uint32_t b) {
   return b >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : (b == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
 }
@@ -135,7 +141,7 @@ CUtensorMapSwizzle swizzle_for_row_bytes(uint32_t b) {
 float alpha_of(const svdq_layer *L) { return L->x_tensor_scale * L->w_tensor_scale; }
 
 HostPipe *host_pipe(DeviceState *d) {
-  HostPipe &p = g_pipe[d - g_dev];
+  HostPipe &p = g_pipe[d->index];
   std::call_once(p.once, [&]() {
     bool ok = cudaStreamCreateWithFlags(&p.in, cudaStreamNonBlocking) == cudaSuccess &&
               cudaStreamCreateWithFlags(&p.out, cudaStreamNonBlocking) == cudaSuccess &&

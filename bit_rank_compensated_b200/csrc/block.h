@@ -1,0 +1,87 @@
+// Launch interfaces of the operators around the projections (layer norm, 8-bit linear, rotary
+// positions) between their C ABI (api_block.cu) and their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "host.h"
+#include "svdq.h"
+
+namespace svdq {
+
+// Rows of X and the weight and bias their layer norm takes.
+struct NormLaunch {
+  const void *X;
+  size_t x_stride;
+  int dtype, M, K;
+  const void *weight, *bias;  // or null
+  size_t weight_stride, bias_stride;
+  int param_dtype, groups, rows_per_group;
+  float weight_offset, eps;
+  // forward
+  void *Y;
+  size_t y_stride;
+  float *mean, *rstd;  // out (forward, may be null) or in (backward)
+  // int8 rows instead of Y
+  int8_t *xq;
+  float *x_scale;
+  // backward
+  const void *dY;
+  size_t dy_stride;
+  void *dX;
+  size_t dx_stride;
+  float *dweight, *dbias;
+  float *partial;  // workspace
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_layer_norm(const NormLaunch &a);
+cudaError_t launch_layer_norm_quantize(const NormLaunch &a);
+cudaError_t launch_layer_norm_backward(const NormLaunch &a);
+size_t layer_norm_partial_bytes(int M, int K, int groups, int rows_per_group);
+
+// int8 rows of X (or of X * col_scale).
+struct QuantRowsLaunch {
+  const void *X;
+  size_t x_stride;
+  int dtype, M, K;
+  const float *col_scale;
+  int8_t *xq;
+  float *x_scale;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_i8_quantize_rows(const QuantRowsLaunch &a);
+
+// Y = (xq wq^T) x_scale w_scale + bias.
+struct I8GemmLaunch {
+  const int8_t *xq, *wq;
+  const float *x_scale, *w_scale, *bias;
+  int M, N, K;
+  void *Y;
+  int y_dtype;
+  void *workspace;
+  const DeviceState *dev;
+  cudaStream_t stream;
+};
+cudaError_t launch_i8_gemm(const I8GemmLaunch &a);
+size_t i8_gemm_workspace_bytes(int M, int N, int K);
+
+// Rotary positions: table, or the heads' rotation.
+struct RopeLaunch {
+  svdq_positions pos;
+  svdq_rope_axes axes;
+  int n_pairs;
+  int M;
+  float *table;
+  svdq_heads in[2], out[2];  // Q and K (heads 0: none)
+  int dtype, head_dim;
+  bool inverse;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_rope_table(const RopeLaunch &a);
+cudaError_t launch_rope_apply(const RopeLaunch &a);
+
+}  // namespace svdq

@@ -33,6 +33,9 @@ EXPORTED = (
     "svdq_awq_packed_weight_bytes", "svdq_awq_packed_sz_bytes", "svdq_prepare_weights_host",
     "svdq_unswizzle_scales", "svdq_test_override_capability", "svdq_mlp_workspace_bytes",
     "svdq_gemm_w4a4_lora_up_gelu_quant", "svdq_gemm_w4a4_lora_up_gelu", "svdq_mlp_forward",
+    "svdq_layer_norm", "svdq_layer_norm_workspace_bytes", "svdq_layer_norm_backward", "svdq_i8_quantize_rows",
+    "svdq_i8_layer_norm_quantize", "svdq_i8_workspace_bytes", "svdq_i8_gemm", "svdq_i8_linear_forward",
+    "svdq_rope_axes_table", "svdq_rope_axes_apply",
 )
 
 
@@ -50,6 +53,29 @@ class LayerStruct(ctypes.Structure):
         ("lambda_", ctypes.c_void_p), ("L1t", ctypes.c_void_p), ("L2t", ctypes.c_void_p),
         ("bias", ctypes.c_void_p),
     ]
+
+
+class NormAffineStruct(ctypes.Structure):
+    _fields_ = [
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("weight_stride", ctypes.c_size_t),
+        ("bias_stride", ctypes.c_size_t), ("dtype", ctypes.c_int32), ("groups", ctypes.c_int32),
+        ("rows_per_group", ctypes.c_int32), ("weight_offset", ctypes.c_float),
+    ]
+
+
+class RopeAxesStruct(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * 4), ("shared_ladder", ctypes.c_int32),
+                ("halves", ctypes.c_int32), ("theta", ctypes.c_float)]
+
+
+class PositionsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("token_stride", ctypes.c_size_t),
+                ("axis_stride", ctypes.c_size_t)]
+
+
+class HeadsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int32), ("token_stride", ctypes.c_size_t),
+                ("head_stride", ctypes.c_size_t)]
 
 
 _lib = None
@@ -99,6 +125,16 @@ def load() -> ctypes.CDLL:
         "svdq_gemm_w4a4_lora_up_gelu_quant": ([P, P, P, I, LP, LP, P, P, P, P, S, P], I),
         "svdq_gemm_w4a4_lora_up_gelu": ([P, P, P, I, LP, P, P], I),
         "svdq_mlp_forward": ([P, I, LP, LP, P, P, P, P, P, P, P, S, P, P], I),
+        "svdq_layer_norm": ([P, S, I, I, I, P, F, P, S, P, P, P], I),
+        "svdq_layer_norm_workspace_bytes": ([I, I, I, I], S),
+        "svdq_layer_norm_backward": ([P, S, P, S, I, I, I, P, P, P, P, S, P, P, P, S, P], I),
+        "svdq_i8_quantize_rows": ([P, S, I, I, I, P, P, P, P], I),
+        "svdq_i8_layer_norm_quantize": ([P, S, I, I, I, P, F, P, P, P], I),
+        "svdq_i8_workspace_bytes": ([I, I, I], S),
+        "svdq_i8_gemm": ([P, P, I, P, P, P, I, I, P, I, P, S, P], I),
+        "svdq_i8_linear_forward": ([P, S, I, I, P, P, P, P, I, I, P, P, P, P, S, P], I),
+        "svdq_rope_axes_table": ([P, I, P, P, P], I),
+        "svdq_rope_axes_apply": ([P, P, P, P, I, I, I, P, P, I, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -469,6 +505,310 @@ def unfused_forward(X, layer, bufs, Y, stream=None):
     if layer.rank:
         baseline_lora_up(la, M, layer, Y, stream)
     return Y
+
+
+# ---------------------------------------------------------------- operators around the projections
+# Unlike the calls above these check what they are given (shapes, types, devices; ValueError), since
+# their rows may be strided views, and run on the tensors' device whichever is current.
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3, torch.int64: 4}
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _run(name: str, device: torch.device, *args):
+    """Calls an entry point on the tensors' device and its current stream."""
+    index = device.index
+    fn = getattr(_lib or load(), name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != SVDQ_OK:
+        _check(name, status)
+
+
+def _rows(t, name: str, dtypes=_FLOATS):
+    """(rows, columns, row stride) of a matrix whose rows are contiguous."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
+    _need(t.dim() == 2, f"{name} must have two dimensions, got {t.dim()}")
+    _need(t.dtype in dtypes, f"{name} has the unsupported type {t.dtype}")
+    M, K = t.shape
+    _need(K <= 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
+    stride = t.stride(0) if M > 1 else K
+    _need(stride >= K, f"the rows of {name} overlap")
+    return M, K, stride
+
+
+def _vector(t, name: str, n: int, device, dtype=torch.float32):
+    """A contiguous vector of n values (or None); its address."""
+    if t is None:
+        return None
+    _need(isinstance(t, torch.Tensor) and t.device == device, f"{name} must be on {device}")
+    _need(t.dtype == dtype and t.numel() == n and t.is_contiguous(), f"{name} must be {n} contiguous {dtype} values")
+    return t.data_ptr()
+
+
+def _on_stream(stream, fn, *args, **kw):
+    """Runs fn with `stream` as the current one, so that what it allocates belongs to that stream."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _norm_affine(X, M: int, K: int, weight, bias, rows_per_group, weight_offset: float):
+    """The C struct of a layer norm's weight and bias ([K] or [groups, K]), and the number of groups."""
+    groups, dtype = 1, torch.float32
+    s = NormAffineStruct()
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        t = t[None] if t.dim() == 1 else t
+        n, k, stride = _rows(t, name)
+        _need(k == K and t.device == X.device, f"{name} must have {K} columns and be on {X.device}")
+        other = bias if name == "weight" else weight
+        _need(other is None or (other.dtype == t.dtype and other.numel() == t.numel()),
+              "weight and bias must have one type and shape")
+        groups, dtype = n, t.dtype
+        setattr(s, name, t.data_ptr())
+        setattr(s, name + "_stride", stride)
+    rows = rows_per_group or max(1, -(-M // max(1, groups)))
+    _need(groups >= 1 and rows >= 1 and groups * rows >= M, f"{groups} groups of {rows} rows do not cover {M} rows")
+    s.dtype, s.groups, s.rows_per_group, s.weight_offset = DTYPES[dtype], groups, rows, weight_offset
+    return s, groups
+
+
+def _like(out, X, shape, dtype, name: str):
+    """A caller's output, checked, or a new one; and its row stride."""
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=X.device)
+        return out, shape[1]
+    M, K, stride = _rows(out, name, (dtype,))
+    _need((M, K) == tuple(shape) and out.device == X.device, f"{name} must be {tuple(shape)} on {X.device}")
+    return out, stride
+
+
+def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset: float = 0.0, eps: float = 1e-6,
+               Y=None, stats: bool = False, stream=None):
+    """Y = (X - mean) * rstd * (weight_offset + weight) + bias over the columns of X [M, K].
+
+    weight, bias: [K], or [groups, K] where row m takes group m // rows_per_group (0: the rows shared out
+    evenly), e.g. the scale and shift of a modulation with weight_offset 1; views of one projection's
+    output will do. Y may be X. With stats also returns mean and rstd (fp32 [M]) for the backward pass."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm, X, weight, bias, rows_per_group, weight_offset, eps, Y, stats)
+    M, K, x_stride = _rows(X, "X")
+    affine, _ = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
+    Y, y_stride = _like(Y, X, (M, K), X.dtype, "Y")
+    mean = torch.empty(M, dtype=torch.float32, device=X.device) if stats else None
+    rstd = torch.empty(M, dtype=torch.float32, device=X.device) if stats else None
+    _run("svdq_layer_norm", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K, ctypes.addressof(affine), eps,
+         Y.data_ptr(), y_stride, mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None)
+    return (Y, mean, rstd) if stats else Y
+
+
+def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0, weight_offset: float = 0.0, dX=None,
+                        groups: int | None = None, need_dX: bool = True, need_dweight: bool = True,
+                        need_dbias: bool = True, workspace=None, stream=None):
+    """(dX, dweight, dbias) of layer_norm for the output's gradient dY; dX of X's type, dweight and dbias
+    fp32 [groups, K]. None in the place of what is not needed. dX may be dY or X. Without a weight,
+    groups gives the number of the bias's groups."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm_backward, dY, X, mean, rstd, weight, rows_per_group, weight_offset, dX,
+                          groups, need_dX, need_dweight, need_dbias, workspace)
+    M, K, x_stride = _rows(X, "X")
+    m, k, dy_stride = _rows(dY, "dY", (X.dtype,))
+    _need((m, k) == (M, K) and dY.device == X.device, "dY must have X's shape and device")
+    affine, n = _norm_affine(X, M, K, weight, None, rows_per_group, weight_offset)
+    if weight is None and groups:
+        n = affine.groups = groups
+        affine.rows_per_group = rows_per_group or max(1, -(-M // groups))
+        _need(groups >= 1 and affine.rows_per_group * groups >= M, f"the groups do not cover {M} rows")
+    _need(groups is None or groups == n, "groups must be the weight's number of rows")
+    dx_stride = K
+    if need_dX:
+        dX, dx_stride = _like(dX, X, (M, K), X.dtype, "dX")
+    else:
+        dX = None
+    dw = torch.empty(n, K, dtype=torch.float32, device=X.device) if need_dweight else None
+    db = torch.empty(n, K, dtype=torch.float32, device=X.device) if need_dbias else None
+    size = load().svdq_layer_norm_workspace_bytes(M, K, n, affine.rows_per_group) if dw is not None or db is not None else 0
+    if size and workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=X.device)
+    _run("svdq_layer_norm_backward", X.device, dY.data_ptr(), dy_stride, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+         ctypes.addressof(affine), _vector(mean, "mean", M, X.device), _vector(rstd, "rstd", M, X.device),
+         None if dX is None else dX.data_ptr(), dx_stride, None if dw is None else dw.data_ptr(),
+         None if db is None else db.data_ptr(), *_workspace(workspace, X.device))
+    return dX, dw, db
+
+
+def _workspace(t, device):
+    if t is None:
+        return None, 0
+    _need(t.device == device and t.is_contiguous(), f"the workspace must be contiguous and on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
+    """(int8 rows, fp32 scale of each) of X [M, K] or of X * col_scale (fp32 [K]): activations by token,
+    weights by output channel."""
+    if stream is not None:
+        return _on_stream(stream, i8_quantize_rows, X, col_scale, xq, x_scale)
+    M, K, x_stride = _rows(X, "X")
+    xq, x_scale = _i8_rows(X, M, K, xq, x_scale)
+    _run("svdq_i8_quantize_rows", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+         _vector(col_scale, "col_scale", K, X.device), xq.data_ptr(), x_scale.data_ptr())
+    return xq, x_scale
+
+
+def _i8_rows(X, M: int, K: int, xq, x_scale):
+    if xq is None:
+        xq = torch.empty(M, K, dtype=torch.int8, device=X.device)
+    else:
+        _vector(xq, "xq", M * K, X.device, torch.int8)
+    if x_scale is None:
+        x_scale = torch.empty(M, dtype=torch.float32, device=X.device)
+    else:
+        _vector(x_scale, "x_scale", M, X.device)
+    return xq, x_scale
+
+
+def i8_layer_norm_quantize(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset: float = 0.0,
+                           eps: float = 1e-6, xq=None, x_scale=None, stream=None):
+    """i8_quantize_rows of the unrounded layer_norm(X, ...), which is not written."""
+    if stream is not None:
+        return _on_stream(stream, i8_layer_norm_quantize, X, weight, bias, rows_per_group, weight_offset, eps, xq,
+                          x_scale)
+    M, K, x_stride = _rows(X, "X")
+    affine, _ = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
+    xq, x_scale = _i8_rows(X, M, K, xq, x_scale)
+    _run("svdq_i8_layer_norm_quantize", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+         ctypes.addressof(affine), eps, xq.data_ptr(), x_scale.data_ptr())
+    return xq, x_scale
+
+
+def i8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return load().svdq_i8_workspace_bytes(M, N, K)
+
+
+def _i8_weight(wq, w_scale, bias, K: int, device):
+    _need(isinstance(wq, torch.Tensor) and wq.dim() == 2 and wq.shape[1] == K, f"wq must have {K} columns")
+    N = wq.shape[0]
+    return N, (_vector(wq, "wq", N * K, device, torch.int8), _vector(w_scale, "w_scale", N, device),
+               _vector(bias, "bias", N, device))
+
+
+def _i8_output(Y, workspace, M: int, N: int, K: int, dtype, device):
+    if Y is None:
+        Y = torch.empty(M, N, dtype=dtype, device=device)
+    else:
+        _vector(Y, "Y", M * N, device, dtype)
+    size = load().svdq_i8_workspace_bytes(M, N, K)
+    if size and workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    return Y, _workspace(workspace, device)
+
+
+def i8_gemm(xq, x_scale, wq, w_scale, bias=None, Y=None, dtype=torch.bfloat16, workspace=None, stream=None):
+    """Y [M, N] = (xq wq^T) * x_scale[:, None] * w_scale + bias from int8 rows, with exact integer sums."""
+    if stream is not None:
+        return _on_stream(stream, i8_gemm, xq, x_scale, wq, w_scale, bias, Y, dtype, workspace)
+    M, K, _ = _rows(xq, "xq", (torch.int8,))
+    _need(xq.is_contiguous() and dtype in _FLOATS, "xq must be contiguous, and dtype a floating type of 16 or 32 bits")
+    N, (w, ws, b) = _i8_weight(wq, w_scale, bias, K, xq.device)
+    Y, space = _i8_output(Y, workspace, M, N, K, dtype, xq.device)
+    _run("svdq_i8_gemm", xq.device, xq.data_ptr(), _vector(x_scale, "x_scale", M, xq.device), M, w, ws, b, N, K,
+         Y.data_ptr(), DTYPES[dtype], *space)
+    return Y
+
+
+def i8_linear_forward(X, wq, w_scale, bias=None, col_scale=None, xq=None, x_scale=None, Y=None, workspace=None,
+                      stream=None):
+    """The 8-bit linear of X [M, K]: rows quantized (under the smoothing col_scale, if any), then i8_gemm;
+    Y has X's type."""
+    if stream is not None:
+        return _on_stream(stream, i8_linear_forward, X, wq, w_scale, bias, col_scale, xq, x_scale, Y, workspace)
+    M, K, x_stride = _rows(X, "X")
+    N, (w, ws, b) = _i8_weight(wq, w_scale, bias, K, X.device)
+    xq, x_scale = _i8_rows(X, M, K, xq, x_scale)
+    Y, space = _i8_output(Y, workspace, M, N, K, X.dtype, X.device)
+    _run("svdq_i8_linear_forward", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M,
+         _vector(col_scale, "col_scale", K, X.device), w, ws, b, N, K, xq.data_ptr(), x_scale.data_ptr(), Y.data_ptr(),
+         *space)
+    return Y
+
+
+class RopeAxes:
+    """How the column pairs of a head are shared out among the axes of a token's position.
+
+    pairs: column pairs of each axis, in order (one to four axes). Each axis has its own ladder of
+    frequencies theta^-(i / pairs[a]), or with shared_ladder all pairs one, theta^-(p / sum(pairs)).
+    Pair p is columns (2p, 2p + 1), or with halves (p, p + sum(pairs))."""
+
+    def __init__(self, pairs, theta: float = 10000.0, shared_ladder: bool = False, halves: bool = False):
+        _need(1 <= len(pairs) <= 4 and min(pairs) >= 1, "one to four axes of at least one pair are supported")
+        self.pairs, self.theta = tuple(pairs), float(theta)
+        self.n_pairs = sum(pairs)
+        self.s = RopeAxesStruct(len(pairs), tuple(pairs), int(shared_ladder), int(halves), theta)
+
+
+def _positions(pos, axes: RopeAxes):
+    _need(isinstance(pos, torch.Tensor) and pos.is_cuda and pos.dtype in (torch.int32, torch.int64, torch.float32),
+          "pos must be a CUDA tensor of int32, int64 or fp32")
+    if pos.dim() == 1:
+        pos = pos[:, None]
+    _need(pos.dim() == 2 and pos.shape[1] == len(axes.pairs), f"pos must be [tokens, {len(axes.pairs)}]")
+    return PositionsStruct(pos.data_ptr(), DTYPES[pos.dtype], pos.stride(0), pos.stride(1))
+
+
+def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
+    """(cos, sin) of every token and pair, fp32 [M, pairs, 2], from position ids [M, axes]: with 64 pairs the
+    table that gemm_w4a4_lora_up_qk_norm_rope and qk_norm_rope take."""
+    if stream is not None:
+        return _on_stream(stream, rope_axes_table, pos, axes, table)
+    p = _positions(pos, axes)
+    M, n = pos.shape[0], axes.n_pairs
+    if table is None:
+        table = torch.empty(M, n, 2, dtype=torch.float32, device=pos.device)
+    _run("svdq_rope_axes_table", pos.device, ctypes.addressof(p), M, ctypes.addressof(axes.s),
+         _vector(table, "table", 2 * M * n, pos.device))
+    return table
+
+
+def _heads(t, out, name: str, like):
+    """The C structs of heads [M, H, D] and of their output (a new one unless given)."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3, f"{name} must be a CUDA tensor [tokens, heads, columns]")
+    _need(t.dtype in _FLOATS and t.dtype == like.dtype and t.device == like.device and t.shape[0] == like.shape[0]
+          and t.shape[2] == like.shape[2], f"{name}'s type, device, tokens or columns differ from what they must be")
+    if out is None:
+        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    _need(out.shape == t.shape and out.dtype == t.dtype and out.device == t.device, f"{name}_out must be like {name}")
+    s = []
+    for v in (t, out):
+        _need(v.stride(2) == 1, f"the columns of {name} must be contiguous")
+        s.append(HeadsStruct(v.data_ptr(), v.shape[1], v.stride(0), v.stride(1)))
+    return s[0], s[1], out
+
+
+def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotates the heads q [M, Hq, D] and k [M, Hk, D] (or None) by the positions pos [M, axes], with no table;
+    with inverse, back: the gradient of the rotation. Views of a packed projection will do; q_out and k_out may
+    be q and k. Returns (q_out, k_out)."""
+    if stream is not None:
+        return _on_stream(stream, rope_axes_apply, q, k, pos, axes, inverse, q_out, k_out)
+    qi, qo, q_out = _heads(q, q_out, "q", q)
+    ki = ko = None
+    if k is not None:
+        ki, ko, k_out = _heads(k, k_out, "k", q)
+    p = _positions(pos, axes)
+    _need(pos.shape[0] == q.shape[0] and pos.device == q.device, "pos must have q's tokens and device")
+    at = ctypes.addressof
+    _run("svdq_rope_axes_apply", q.device, at(qi), at(qo), None if k is None else at(ki), None if k is None else at(ko),
+         DTYPES[q.dtype], q.shape[0], q.shape[2], at(p), at(axes.s), int(inverse))
+    return q_out, (None if k is None else k_out)
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:

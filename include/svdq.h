@@ -299,6 +299,141 @@ SVDQ_API svdq_status svdq_awq_pack_weights(const uint8_t *wq, const uint16_t *sc
 SVDQ_API svdq_status svdq_awq_gemv_w4a16(const uint16_t *X, int M, const uint8_t *wq_packed, const uint8_t *sz_packed,
                                          const float *bias, int N, int K, uint16_t *Y, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around the projections of a transformer block: the modulated layer norm in front of
+ * them, an 8-bit linear for the layers that 4 bits do not suit, and the rotary positions behind
+ * the Q and K projections. Activations are bf16, fp16 or fp32 (svdq_dtype); sums, statistics and
+ * angles are held in 32 bits or more and every output is rounded once.
+ *
+ * Pointers of these calls are device pointers aligned to their element (16 bytes where stated;
+ * SVDQ_ERR_MISALIGNED otherwise); rows need not be contiguous: a stride is the distance of two
+ * rows in elements. An output may be an input's own buffer (same address and strides) where
+ * stated; otherwise buffers do not overlap. */
+typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_F16 = 1, SVDQ_F32 = 2, SVDQ_I32 = 3, SVDQ_I64 = 4 } svdq_dtype;
+
+/* Weight and bias of a layer norm, one row of K values for each group of consecutive rows of X
+ * (a batch's samples, each under its own shift and scale, or one group for a plain weight).
+ * Row m of X takes row m / rows_per_group; groups * rows_per_group >= M. */
+typedef struct svdq_norm_affine {
+  const void *weight; /* groups rows of K, or NULL: factor 1 */
+  const void *bias;   /* groups rows of K, or NULL: 0 */
+  size_t weight_stride, bias_stride; /* elements between the groups' rows */
+  int32_t dtype;          /* SVDQ_BF16, SVDQ_F16 or SVDQ_F32 */
+  int32_t groups;         /* >= 1 */
+  int32_t rows_per_group; /* >= 1 */
+  float weight_offset;    /* added to weight: 1 for a modulation's scale, 0 for a norm's weight */
+} svdq_norm_affine;
+
+/* Layer norm over the K columns of every row, with statistics in fp32:
+ *   xhat = (x - mean) * rstd,  mean = sum(x) / K,  rstd = 1 / sqrt(sum((x - mean)^2) / K + eps)
+ *   Y    = xhat * (weight_offset + weight) + bias
+ *   X, Y    device, M x K of dtype (Y may be X).
+ *   affine  host struct, or NULL for Y = xhat.
+ *   mean, rstd  device, M fp32 each, or NULL (kept for the backward pass).
+ * 1 <= K <= 16384, M >= 0 (0: nothing to do), strides >= K, eps >= 0. Asynchronous on stream. */
+SVDQ_API svdq_status svdq_layer_norm(const void *X, size_t x_stride, int dtype, int M, int K,
+                                     const svdq_norm_affine *affine, float eps, void *Y, size_t y_stride,
+                                     float *mean, float *rstd, void *stream);
+
+/* Workspace (device bytes) of svdq_layer_norm_backward: the column sums of each slice of rows. */
+SVDQ_API size_t svdq_layer_norm_workspace_bytes(int M, int K, int groups, int rows_per_group);
+
+/* Gradient of svdq_layer_norm. With g = dY * (weight_offset + weight):
+ *   dX      = rstd * (g - sum(g) / K - xhat * sum(g * xhat) / K)
+ *   dweight = the sum over each group's rows of dY * xhat,  dbias = that of dY
+ * (fp32, groups x K each, contiguous; a group without rows gets zeros). The column sums are formed
+ * in a fixed order: the same call gives the same bits.
+ *   mean, rstd  device, as svdq_layer_norm wrote them for X.
+ *   dX          device, M x K of dtype, or NULL; may be dY or X.
+ *   dweight, dbias  device, or NULL. affine gives groups and rows_per_group (NULL: one group).
+ *   workspace   device, 16-byte aligned, at least svdq_layer_norm_workspace_bytes(...) bytes;
+ *               may be NULL when dweight and dbias are. Contents not kept.
+ * Limits as svdq_layer_norm. Asynchronous on stream. */
+SVDQ_API svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, const void *X, size_t x_stride,
+                                              int dtype, int M, int K, const svdq_norm_affine *affine,
+                                              const float *mean, const float *rstd, void *dX, size_t dx_stride,
+                                              float *dweight, float *dbias, void *workspace,
+                                              size_t workspace_bytes, void *stream);
+
+/* 8-bit linear: Y = (xq wq^T) * x_scale[m] * w_scale[n] + bias[n], with int8 rows, one fp32 scale
+ * for each token and each output channel, and exact 32-bit integer sums. Int8 matrices are
+ * contiguous and 16-byte aligned; K % 16 == 0, N % 16 == 0, K <= 131072 (the largest sum fits
+ * 32 bits). Rows are tokens (activations) or output channels (weights).
+ *
+ * svdq_i8_quantize_rows: for every row, with xhat = fp32(x * col_scale) (col_scale NULL: xhat = x):
+ *   scale = fp32(max|xhat| / 127);  q = rint(127 xhat / max|xhat|), decided on the exact quotient,
+ *   ties to even. A row of zeros gets scale 0 and zeros. A row with an infinity or a NaN gets scale
+ *   NaN and zeros, so that its outputs are NaN.
+ *     X          device, M x K of dtype.
+ *     col_scale  device, K fp32, or NULL: a smoothing of the channels (1 / lambda for tokens, lambda
+ *                for the weight's rows; svdq_smoothing_factors_noalloc).
+ *     xq         device, M x K int8;  x_scale  device, M fp32.
+ * svdq_i8_layer_norm_quantize: the same of the unrounded output of svdq_layer_norm (K <= 16384).
+ * svdq_i8_gemm: the product.  Y device, M x N of y_dtype, contiguous, 16-byte aligned.
+ *     workspace  device, 16-byte aligned, at least svdq_i8_workspace_bytes(M, N, K) bytes (may be 0,
+ *                then NULL is fine): partial sums where few tokens leave the K axis to be split.
+ * svdq_i8_linear_forward: svdq_i8_quantize_rows, then svdq_i8_gemm with Y of X's dtype; xq and
+ *     x_scale are scratch of the sizes above.
+ * M >= 0 (0: nothing to do). Asynchronous on stream. */
+SVDQ_API svdq_status svdq_i8_quantize_rows(const void *X, size_t x_stride, int dtype, int M, int K,
+                                           const float *col_scale, int8_t *xq, float *x_scale, void *stream);
+SVDQ_API svdq_status svdq_i8_layer_norm_quantize(const void *X, size_t x_stride, int dtype, int M, int K,
+                                                 const svdq_norm_affine *affine, float eps, int8_t *xq,
+                                                 float *x_scale, void *stream);
+SVDQ_API size_t svdq_i8_workspace_bytes(int M, int N, int K);
+SVDQ_API svdq_status svdq_i8_gemm(const int8_t *xq, const float *x_scale, int M, const int8_t *wq,
+                                  const float *w_scale, const float *bias, int N, int K, void *Y, int y_dtype,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+SVDQ_API svdq_status svdq_i8_linear_forward(const void *X, size_t x_stride, int dtype, int M, const float *col_scale,
+                                            const int8_t *wq, const float *w_scale, const float *bias, int N, int K,
+                                            int8_t *xq, float *x_scale, void *Y, void *workspace,
+                                            size_t workspace_bytes, void *stream);
+
+/* Rotary positions with several axes (time, height, width of an image's or a video's tokens): the
+ * P = pairs[0] + .. + pairs[n_axes - 1] column pairs of a head are shared out among the axes in
+ * order, and pair p of axis a turns by
+ *   angle = pos[m][a] * theta^-(i / pairs[a]), i = p's index within its axis (a ladder for each axis),
+ *   or pos[m][a] * theta^-(p / P) with shared_ladder (one ladder over all pairs),
+ * formed in fp64. Pair p is columns (2p, 2p + 1), or (p, p + P) with halves. */
+typedef struct svdq_rope_axes {
+  int32_t n_axes;        /* 1 to 4 */
+  int32_t pairs[4];      /* >= 1 for each axis; P <= 256 */
+  int32_t shared_ladder; /* 0 or 1 */
+  int32_t halves;        /* 0 or 1 */
+  float theta;           /* > 0 */
+} svdq_rope_axes;
+
+/* Position ids: pos[m * token_stride + a * axis_stride], int32, int64 or fp32. */
+typedef struct svdq_positions {
+  const void *data;
+  int32_t dtype; /* SVDQ_I32, SVDQ_I64 or SVDQ_F32 */
+  size_t token_stride, axis_stride;
+} svdq_positions;
+
+/* Heads of M tokens: element (m, h, d) at data[m * token_stride + h * head_stride + d]; a section of
+ * a packed projection's rows, or a tensor of its own. */
+typedef struct svdq_heads {
+  void *data;
+  int32_t heads;
+  size_t token_stride, head_stride;
+} svdq_heads;
+
+/* The table that svdq_gemm_w4a4_lora_up_qk_norm_rope and svdq_qk_norm_rope read (for them P = 64):
+ * table[m][p] = (cos, sin), fp32, device, M x P x 2 (8-byte aligned). Asynchronous on stream. */
+SVDQ_API svdq_status svdq_rope_axes_table(const svdq_positions *pos, int M, const svdq_rope_axes *axes, float *table,
+                                          void *stream);
+
+/* Rotates the Q and K heads of M tokens from their position ids, with no table:
+ *   (u0, u1) -> (u0 cos - u1 sin, u1 cos + u0 sin) for every pair; with inverse the angle is negated,
+ *   which undoes the rotation and is its gradient. Columns from 2 P on are copied.
+ *   q, k        inputs (k NULL: Q alone), of dtype; heads and strides may differ (shared K heads).
+ *   q_out, k_out  outputs, the same number of heads; may be the inputs themselves (same strides).
+ * head_dim even, 2 P <= head_dim <= 512; at most 65536 heads; strides >= head_dim; M >= 0. Asynchronous on stream. */
+SVDQ_API svdq_status svdq_rope_axes_apply(const svdq_heads *q, const svdq_heads *q_out, const svdq_heads *k,
+                                          const svdq_heads *k_out, int dtype, int M, int head_dim,
+                                          const svdq_positions *pos, const svdq_rope_axes *axes, int inverse,
+                                          void *stream);
+
 /* K1 then K2 on the same stream (the layer's forward pass). Buffers as above. */
 SVDQ_API svdq_status svdq_linear_forward(const uint16_t *X, int M, const svdq_layer *layer,
                                 uint8_t *xq, uint8_t *xs, uint16_t *lora_act,
