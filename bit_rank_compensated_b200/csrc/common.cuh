@@ -13,7 +13,7 @@ namespace svdq {
 // ---------------------------------------------------------------- error word
 // A kernel that gives up on a bounded wait records (kernel << 16) | (site << 8) | 1 into the
 // library's device error word (first error wins) and leaves its loops.
-enum KernelId : uint32_t { KID_QUANT = 1, KID_GEMM = 2, KID_PREP = 3, KID_BASE = 4, KID_SELFTEST = 5, KID_AWQ = 6 };
+enum KernelId : uint32_t { KID_QUANT = 1, KID_GEMM = 2, KID_PREP = 3, KID_BASE = 4, KID_SELFTEST = 5, KID_AWQ = 6, KID_I8 = 7 };
 
 // About two seconds of %globaltimer (ns) before a wait is declared lost.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -337,6 +337,15 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D (int32) (+)= A B^T of int8 operands, K = 32 (kind::i8).
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

@@ -1,0 +1,331 @@
+// The 8-bit linear's product: Y[m, n] = (sum_k xq[m, k] wq[n, k]) x_scale[m] w_scale[n] + bias[n], with
+// exact 32-bit integer sums.
+//
+// Persistent kernel of CTA pairs (clusters of two CTAs on two SMs). A pair owns an output tile of
+// 256 tokens x BN channels and computes it with cta_group::2 kind::i8 tensor-core MMAs of M = 256,
+// N = BN, K = 32: each CTA stages its own 128 rows of xq and its own BN / 2 rows of wq, 128 columns
+// of K per pipeline step (128-byte rows, 128B swizzle), the even CTA issues the MMAs for both, and
+// each CTA's tensor memory holds the sums of its 128 tokens. Two accumulators (2 BN of the 512
+// tensor-memory columns) let the output stage drain one tile while the next one's MMAs run.
+//
+// The scales multiply the sum once per element, in the output stage: the integer part of the
+// product needs no scale, so int8 runs with no scale traffic in the loop (the 4-bit GEMM's blocks).
+//
+// Warp roles (384 threads): warp 0 TMA producer; warp 1 tensor-memory owner and, in the even CTA,
+// MMA issuer; warps 2, 3 idle; warps 4..11 output stage, two groups of four warps, each one half of
+// the tile's columns (one group for BN = 64). An output thread owns a row (32 lanes per warp and
+// sub-partition), scales it, rounds once, and writes 128-byte rows of a swizzled box that a TMA
+// store clips to M and N. Every wait is bounded.
+#include <atomic>
+#include <type_traits>
+
+#include "block.h"
+#include "common.cuh"
+#include "types.cuh"
+
+namespace svdq {
+namespace {
+
+constexpr int BM = 128;  // tokens per CTA, 256 per pair
+constexpr int STEP = 128;  // columns of K per pipeline step
+constexpr int THREADS = 384;
+constexpr int EPI_WARP0 = 4;
+constexpr uint32_t A_BYTES = BM * STEP;
+constexpr uint32_t BOX_BYTES = BM * 128;  // output box: 128 rows of 128 bytes
+constexpr uint32_t TMEM_COLS = 512;
+
+template <int BN>
+struct Tile {
+  static constexpr int STAGES = BN == 256 ? 5 : (BN == 128 ? 7 : 9);
+  static constexpr uint32_t B_BYTES = BN / 2 * STEP;
+  static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int GROUPS = BN >= 128 ? 2 : 1;  // output groups of four warps
+  static constexpr int COLS = BN / GROUPS;          // columns of a group
+  static constexpr uint32_t DATA_BYTES = STAGES * STAGE_BYTES;
+  static constexpr uint32_t SCALE_BYTES = 2 * 2 * BN * 4;  // w_scale and bias of the tile, two tiles
+  static constexpr int N_BARS = 2 * STAGES + 4;
+  static constexpr uint32_t SMEM = DATA_BYTES + GROUPS * BOX_BYTES + SCALE_BYTES + 256 + 1024;
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+  static_assert(N_BARS * 8 + 4 <= 256, "barrier area");
+  static_assert(STAGE_BYTES % 1024 == 0, "stages keep the 1 KiB alignment of 128B-swizzled tiles");
+};
+
+struct GArgs {
+  const float *x_scale, *w_scale, *bias;
+  int M, N, K;
+  int Mt, Nt;
+  uint32_t *err;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A value from its sum: scaled in fp32, one fp32 rounding each for the sum, the two scales and the bias.
+__device__ __forceinline__ float scaled(int acc, float xs, float ws, float b) {
+  return fmaf(__fmul_rn(static_cast<float>(acc), xs), ws, b);
+}
+
+template <int BN, typename T>
+__global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
+    k_i8_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+              const __grid_constant__ CUtensorMap tm_y, GArgs a) {
+  using C = Tile<BN>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *box_s = smem + C::DATA_BYTES;
+  float *scale_s = reinterpret_cast<float *>(box_s + C::GROUPS * BOX_BYTES);  // [tile parity][w_scale, bias][BN]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(scale_s) + C::SCALE_BYTES);
+  // full[s] (even CTA): stage s is loaded in both CTAs; empty[s]: the MMAs that read it are done (both
+  // CTAs); accfull[b]: accumulator b is complete (both CTAs); accempty[b] (even CTA): both CTAs have read it
+  const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * ST;
+  const uint32_t bar_accfull = bar_empty + 8 * ST, bar_accempty = bar_accfull + 16;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::N_BARS);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const int pid = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int steps = (a.K + STEP - 1) / STEP;
+  const int tiles = a.Mt * a.Nt;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_accfull + 8 * b, 1);
+      mbar_init(bar_accempty + 8 * b, 2 * 4 * C::GROUPS);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+  // global memory only from here on: the prologue overlaps the previous kernel of the stream
+  grid_dep_wait();
+  grid_dep_launch();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_x);
+      tma_prefetch_desc(&tm_w);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pid; t < tiles && ok; t += npairs) {
+        const int row0 = (t % a.Mt) * 2 * BM + static_cast<int>(crank) * BM;
+        const int wrow0 = (t / a.Mt) * BN + static_cast<int>(crank) * (BN / 2);
+        for (int j = 0; j < steps; ++j, ++it) {
+          const int s = it % ST;
+          if (it >= ST && !mbar_wait_parked(bar_empty + 8 * s, ((it / ST) - 1) & 1, a.err, KID_I8, 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t lead = map_shared_rank(bar_full + 8 * s, 0);
+          const uint32_t at = smem_u32(smem + s * C::STAGE_BYTES);
+          if (crank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * C::STAGE_BYTES);
+          tma_load_2d_pair(at, &tm_x, j * STEP, row0, lead);
+          tma_load_2d_pair(at + A_BYTES, &tm_w, j * STEP, wrow0, lead);
+        }
+      }
+      // the MMA issuer's last commits to this CTA's barriers have landed before it exits
+      for (uint32_t i = it > ST ? it - ST : 0; ok && i < it; ++i)
+        ok = mbar_wait(bar_empty + 8 * (i % ST), (i / ST) & 1, a.err, KID_I8, 2);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (crank == 0) {
+      // kind::i8: D int32 (bits 4-5 = 2), A and B int8 (bits 7-9, 10-12 = 1), K-major, N (bits 17-22),
+      // M = 256 across the pair (bits 24-28)
+      constexpr uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t(BN) >> 3) << 17) | ((256u >> 4) << 24);
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int t = pid; t < tiles && ok; t += npairs, ++n) {
+        const uint32_t b = n & 1;
+        if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar_accempty + 8 * b, ((n >> 1) - 1) & 1, a.err, KID_I8, 3))) break;
+        tc_fence_after();
+        for (int j = 0; j < steps; ++j, ++it) {
+          const int s = it % ST;
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * s, (it / ST) & 1, a.err, KID_I8, 4))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + s * C::STAGE_BYTES);
+          const uint64_t ad = umma_desc(at, 16, 1024, 2), bd = umma_desc(at + A_BYTES, 16, 1024, 2);
+          const int kb = min(4, (a.K - j * STEP + 31) / 32);  // columns beyond K are zeros: whole MMAs of them are left out
+          if (elect_one()) {
+            for (int k = 0; k < kb; ++k)
+              mma_i8_pair(tbase + b * BN, ad + 2u * k, bd + 2u * k, idesc, (j | k) != 0 ? 1u : 0u);
+            tc_commit_pair_mc(bar_empty + 8 * s, 0x3);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) tc_commit_pair_mc(bar_accfull + 8 * b, 0x3);
+        __syncwarp();
+      }
+      // the output stages of both CTAs have released the last accumulators
+      for (uint32_t i = n > 2 ? n - 2 : 0; ok && i < n; ++i)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_accempty + 8 * (i & 1), (i >> 1) & 1, a.err, KID_I8, 5));
+    }
+  } else if (warp >= EPI_WARP0 && (warp - EPI_WARP0) / 4 < C::GROUPS) {
+    // ------------------------------------------------------------ output stage
+    const int group = (warp - EPI_WARP0) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const int et = (static_cast<int>(threadIdx.x) - EPI_WARP0 * 32) & 127;  // thread of the group
+    const uint32_t tlane = static_cast<uint32_t>(quad * 32) << 16;
+    constexpr int PER_BOX = 128 / sizeof(T);  // columns of a box
+    uint8_t *rowp = box_s + group * BOX_BYTES + row * 128;
+    const uint32_t box = smem_u32(box_s + group * BOX_BYTES);
+    bool ok = true;
+    uint32_t n = 0;
+    for (int t = pid; t < tiles; t += npairs, ++n) {
+      const uint32_t b = n & 1;
+      const int row0 = (t % a.Mt) * 2 * BM + static_cast<int>(crank) * BM;
+      const int n0 = (t / a.Mt) * BN + group * C::COLS;
+      // this tile's scales and bias: the other parity's copy may still be read by the group's slower warps
+      float *ws = scale_s + b * 2 * BN + group * C::COLS, *bs = ws + BN;
+      if (et < C::COLS) {
+        ws[et] = n0 + et < a.N ? __ldg(a.w_scale + n0 + et) : 0.0f;
+        bs[et] = a.bias && n0 + et < a.N ? __ldg(a.bias + n0 + et) : 0.0f;
+      }
+      const float xs = row0 + row < a.M ? __ldg(a.x_scale + row0 + row) : 0.0f;
+      named_bar_sync(1 + group, 128);
+      if (ok) ok = mbar_wait_parked(bar_accfull + 8 * b, (n >> 1) & 1, a.err, KID_I8, 6);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const uint32_t taddr = tbase + tlane + b * BN + group * C::COLS;
+#pragma unroll 1
+      for (int c = 0; c < C::COLS; c += PER_BOX) {
+        // the box is free once the copy unit has read it
+        if (et == 0) bulk_wait_read0();
+        named_bar_sync(1 + group, 128);
+#pragma unroll
+        for (int h = 0; h < PER_BOX; h += 32) {
+          uint32_t r[32];
+          if (ok) {
+            tmem_ld32(taddr + c + h, r);
+            tmem_wait_ld_dep(r);
+          }
+          if (c + h + 32 == C::COLS) {
+            // the sums are in registers: the accumulator goes back to the MMAs
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(map_shared_rank(bar_accempty + 8 * b, 0));
+          }
+          constexpr int PER16 = 16 / sizeof(T);  // columns per 16 bytes
+#pragma unroll
+          for (int q = 0; q < 32 / PER16; ++q) {
+            uint32_t w[4];
+            float v[PER16];
+#pragma unroll
+            for (int e = 0; e < PER16; e += 4) {
+              const float4 w4 = *reinterpret_cast<const float4 *>(ws + c + h + q * PER16 + e);
+              const float4 b4 = *reinterpret_cast<const float4 *>(bs + c + h + q * PER16 + e);
+              v[e] = scaled(static_cast<int>(r[q * PER16 + e]), xs, w4.x, b4.x);
+              v[e + 1] = scaled(static_cast<int>(r[q * PER16 + e + 1]), xs, w4.y, b4.y);
+              v[e + 2] = scaled(static_cast<int>(r[q * PER16 + e + 2]), xs, w4.z, b4.z);
+              v[e + 3] = scaled(static_cast<int>(r[q * PER16 + e + 3]), xs, w4.w, b4.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(v[e]);
+              else w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+            }
+            const int ch = h / PER16 + q;
+            *reinterpret_cast<uint4 *>(rowp + ((ch ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(1 + group, 128);
+        if (et == 0) {
+          if (ok && n0 + c < a.N && row0 < a.M) tma_store_2d(&tm_y, box, n0 + c, row0);
+          bulk_commit();
+        }
+      }
+    }
+    if (et == 0) bulk_wait0();  // stores complete before the CTA exits
+  }
+
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync_all();  // neither CTA frees the pair's tensor memory while the other still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, TMEM_COLS);
+  }
+}
+
+template <int BN, typename T>
+cudaError_t launch_pair(const I8GemmLaunch &g) {
+  using C = Tile<BN>;
+  CUtensorMap tx, tw, ty;
+  const uint64_t K = g.K, e = sizeof(T);
+  constexpr CUtensorMapDataType dt = sizeof(T) == 4              ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : std::is_same_v<T, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.xq, K, g.M, K, STEP, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.wq, K, g.N, K, STEP, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&ty, dt, g.Y, g.N, g.M, g.N * e, 128 / e, BM, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  GArgs a{g.x_scale, g.w_scale, g.bias, g.M, g.N, g.K, (g.M + 2 * BM - 1) / (2 * BM), (g.N + BN - 1) / BN, g.dev->err};
+  auto kern = k_i8_gemm<BN, T>;
+  // once per device and instance; setting it again is harmless, so no lock
+  static std::atomic<bool> ready[64];
+  if (!ready[g.dev->index].load(std::memory_order_acquire)) {
+    const cudaError_t e2 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e2 != cudaSuccess) return e2;
+    ready[g.dev->index].store(true, std::memory_order_release);
+  }
+  const int64_t tiles = static_cast<int64_t>(a.Mt) * a.Nt;
+  const int slots = g.dev->num_sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < slots ? tiles : slots), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = g.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tx, tw, ty, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const I8GemmLaunch &g) {
+  const int slots = g.dev->num_sms / 2;
+  const int64_t mt = (g.M + 2 * BM - 1) / (2 * BM);
+  auto waves = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + slots - 1) / slots; };
+  // the widest tile whose waves take no longer than a narrower one's
+  if (waves(256) * 256 <= waves(128) * 160 && waves(256) * 256 <= waves(64) * 112) return launch_pair<256, T>(g);
+  if (waves(128) * 160 <= waves(64) * 112) return launch_pair<128, T>(g);
+  return launch_pair<64, T>(g);
+}
+
+}  // namespace
+
+size_t i8_gemm_workspace_bytes(int, int, int) { return 0; }
+
+cudaError_t launch_i8_gemm(const I8GemmLaunch &g) {
+  if (static_cast<int64_t>((g.M + 2 * BM - 1) / (2 * BM)) * ((g.N + 63) / 64) >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (g.y_dtype == SVDQ_F32) return launch_t<float>(g);
+  if (g.y_dtype == SVDQ_F16) return launch_t<__half>(g);
+  return launch_t<__nv_bfloat16>(g);
+}
+
+}  // namespace svdq
