@@ -9,6 +9,7 @@ using namespace svdq;
 
 namespace {
 
+constexpr int kMaxRows = 1 << 30;
 constexpr int kMaxNormColumns = 16384;
 constexpr int kMaxHeads = 65536;
 constexpr int kMaxI8Columns = 131072;  // 127 * 127 * K < 2^31
@@ -34,7 +35,7 @@ svdq_status done(cudaError_t e) { return e == cudaSuccess ? SVDQ_OK : SVDQ_ERR_C
 svdq_status norm_args(const void *X, size_t x_stride, int dtype, int M, int K, const svdq_norm_affine *af, float eps,
                       NormLaunch *a) {
   memset(a, 0, sizeof(*a));
-  if (!is_float(dtype) || M < 0 || K < 1 || K > kMaxNormColumns || x_stride < static_cast<size_t>(K))
+  if (!is_float(dtype) || M < 0 || M > kMaxRows || K < 1 || K > kMaxNormColumns || x_stride < static_cast<size_t>(K))
     return SVDQ_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !isfinite(eps)) return SVDQ_ERR_INVALID_ARG;
   if (!X && M > 0) return SVDQ_ERR_INVALID_ARG;
@@ -70,7 +71,7 @@ svdq_status norm_args(const void *X, size_t x_stride, int dtype, int M, int K, c
 
 svdq_status check_axes(const svdq_positions *pos, int M, const svdq_rope_axes *ax, RopeLaunch *a) {
   memset(static_cast<void *>(a), 0, sizeof(*a));
-  if (!pos || !ax || M < 0 || ax->n_axes < 1 || ax->n_axes > 4) return SVDQ_ERR_INVALID_ARG;
+  if (!pos || !ax || M < 0 || M > kMaxRows || ax->n_axes < 1 || ax->n_axes > 4) return SVDQ_ERR_INVALID_ARG;
   int P = 0;
   for (int i = 0; i < ax->n_axes; ++i) {
     if (ax->pairs[i] < 1 || ax->pairs[i] > 256) return SVDQ_ERR_INVALID_ARG;
@@ -90,7 +91,7 @@ svdq_status check_axes(const svdq_positions *pos, int M, const svdq_rope_axes *a
 svdq_status check_gemm(const int8_t *xq, const float *x_scale, int M, const int8_t *wq, const float *w_scale,
                        const float *bias, int N, int K, const void *Y, int y_dtype, const void *workspace,
                        size_t workspace_bytes) {
-  if (!is_float(y_dtype) || M < 0 || N < 16 || N % 16 || K < 16 || K % 16 || K > kMaxI8Columns)
+  if (!is_float(y_dtype) || M < 0 || M > kMaxRows || N < 16 || N % 16 || K < 16 || K % 16 || K > kMaxI8Columns)
     return SVDQ_ERR_INVALID_ARG;
   if (!wq || !w_scale || (M > 0 && (!xq || !x_scale || !Y))) return SVDQ_ERR_INVALID_ARG;
   const size_t need = svdq_i8_workspace_bytes(M, N, K);
@@ -180,7 +181,7 @@ svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, const voi
 
 svdq_status svdq_i8_quantize_rows(const void *X, size_t x_stride, int dtype, int M, int K, const float *col_scale,
                                   int8_t *xq, float *x_scale, void *stream) {
-  if (!is_float(dtype) || M < 0 || K < 16 || K % 16 || K > kMaxI8Columns || x_stride < static_cast<size_t>(K))
+  if (!is_float(dtype) || M < 0 || M > kMaxRows || K < 16 || K % 16 || K > kMaxI8Columns || x_stride < static_cast<size_t>(K))
     return SVDQ_ERR_INVALID_ARG;
   if (M > 0 && (!X || !xq || !x_scale)) return SVDQ_ERR_INVALID_ARG;
   if (!aligned(X, elem_bytes(dtype)) || !aligned(col_scale, 4) || !aligned16(xq) || !aligned(x_scale, 4))

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "host.h"
 #include "svdq.h"
 
@@ -83,5 +85,23 @@ struct RopeLaunch {
 };
 cudaError_t launch_rope_table(const RopeLaunch &a);
 cudaError_t launch_rope_apply(const RopeLaunch &a);
+
+// Launches a kernel that waits (grid_dep_wait) before it touches global memory, so that its start may
+// overlap the end of the stream's previous kernel.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                             std::type_identity_t<Args>... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 }  // namespace svdq

@@ -293,17 +293,8 @@ cudaError_t launch_pair(const I8GemmLaunch &g) {
   }
   const int64_t tiles = static_cast<int64_t>(a.Mt) * a.Nt;
   const int slots = g.dev->num_sms / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < slots ? tiles : slots), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = g.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tx, tw, ty, a);
+  const dim3 grid(2 * static_cast<unsigned>(tiles < slots ? tiles : slots));
+  return launch_dependent(kern, grid, THREADS, C::SMEM, g.stream, tx, tw, ty, a);
 }
 
 template <typename T>

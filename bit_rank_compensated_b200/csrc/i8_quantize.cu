@@ -1,32 +1,82 @@
-// Int8 rows with one scale each, of X or of X under a smoothing of its columns.
+// Int8 rows with one scale each, of X or of X under a smoothing of its columns. Bound by memory: a row of
+// up to 16384 values is read once into the registers of a block (row.cuh), which finds its maximum and
+// writes its codes; a longer one is read a second time, from L2.
 #include "block.h"
+#include "common.cuh"
 #include "i8_quant.cuh"
-#include "types.cuh"
+#include "row.cuh"
 
 namespace svdq {
 namespace {
 
-constexpr int kThreads = 256;
+template <typename T, int TEAM, int E, int VEC>
+__global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_quantize_rows(QuantRowsLaunch a, int rows_per_block) {
+  __shared__ BlockMax<TEAM> top;
+  grid_dep_wait();
+  grid_dep_launch();
+  uint32_t turn = 0;
+  const int m0 = blockIdx.x * rows_per_block;
+  const int m1 = min(a.M, m0 + rows_per_block);
+  const T *x0 = static_cast<const T *>(a.X);
+  RawRow<T, TEAM, VEC, E> next;
+  if (m0 < m1) next.load(x0 + m0 * a.x_stride, a.K);
+  float c[E];
+  if (a.col_scale) load_params<TEAM, VEC, E>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
+  for (int m = m0; m < m1; ++m) {
+    float x[E];
+    next.values(x);
+    if (m + 1 < m1) next.load(x0 + (m + 1) * a.x_stride, a.K);
+    uint32_t t = 0;  // columns beyond K are zeros
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (a.col_scale) x[i] = __fmul_rn(x[i], c[i]);
+      t = max(t, abs_bits(x[i]));
+    }
+    const RowScale r = row_scale(top(t, turn));
+    if (threadIdx.x == 0) a.x_scale[m] = r.scale;
+    int q[E];
+    i8_codes<E>(x, r, q);
+    store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, q);
+  }
+}
 
+// Rows of any length, read twice.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_quantize_rows(QuantRowsLaunch a) {
+__global__ void __launch_bounds__(1024) k_quantize_long_rows(QuantRowsLaunch a) {
+  __shared__ BlockMax<1024> top;
   const size_t m = blockIdx.x;
   const T *x = static_cast<const T *>(a.X) + m * a.x_stride;
   auto value = [&](int k) { return a.col_scale ? __fmul_rn(to_f32(x[k]), a.col_scale[k]) : to_f32(x[k]); };
-  uint32_t top = 0;
-  for (int k = threadIdx.x; k < a.K; k += kThreads) top = max(top, abs_bits(value(k)));
-  const RowScale r = row_scale(block_max<kThreads>(top));
+  uint32_t t = 0, turn = 0;
+  for (int k = threadIdx.x; k < a.K; k += 1024) t = max(t, abs_bits(value(k)));
+  const RowScale r = row_scale(top(t, turn));
   if (threadIdx.x == 0) a.x_scale[m] = r.scale;
-  for (int k = threadIdx.x; k < a.K; k += kThreads) a.xq[m * a.K + k] = i8_code(value(k), r);
+  for (int k = threadIdx.x; k < a.K; k += 1024) a.xq[m * a.K + k] = static_cast<int8_t>(i8_code(value(k), r));
+}
+
+template <typename T>
+cudaError_t quantize_t(const QuantRowsLaunch &a) {
+  if (a.K > kMaxRow) {
+    k_quantize_long_rows<T><<<a.M, 1024, 0, a.stream>>>(a);
+    return cudaGetLastError();
+  }
+  const bool vec = a.K % kVec<T> == 0 && rows_aligned(a.X, a.M > 1 ? a.x_stride : 0, sizeof(T), 16) &&
+                   rows_aligned(a.col_scale, 0, 4, 16);
+  return for_row(a.K, [&]<int TEAM, int E>() {
+    const int blocks = a.num_sms * kBlocksPerSm<TEAM>;
+    const int rows = (a.M + blocks - 1) / blocks;
+    const dim3 grid((a.M + rows - 1) / rows);
+    if (vec) return launch_dependent(k_quantize_rows<T, TEAM, E, kVec<T>>, grid, TEAM, 0, a.stream, a, rows);
+    return launch_dependent(k_quantize_rows<T, TEAM, E, 1>, grid, TEAM, 0, a.stream, a, rows);
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_i8_quantize_rows(const QuantRowsLaunch &a) {
-  if (a.dtype == SVDQ_F32) k_quantize_rows<float><<<a.M, kThreads, 0, a.stream>>>(a);
-  else if (a.dtype == SVDQ_F16) k_quantize_rows<__half><<<a.M, kThreads, 0, a.stream>>>(a);
-  else k_quantize_rows<__nv_bfloat16><<<a.M, kThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  if (a.dtype == SVDQ_F32) return quantize_t<float>(a);
+  if (a.dtype == SVDQ_F16) return quantize_t<__half>(a);
+  return quantize_t<__nv_bfloat16>(a);
 }
 
 }  // namespace svdq

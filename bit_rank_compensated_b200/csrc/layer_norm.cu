@@ -1,150 +1,291 @@
 // Layer norm with a weight and a bias for each group of rows, its int8 output form and its gradient.
+//
+//   xhat = (x - mean) rstd,  y = xhat (offset + w) + b;  dx = rstd (g - mean(g) - xhat mean(g xhat)),
+//   g = dy (offset + w);  dw = sum over rows of dy xhat,  db = sum over rows of dy.
+//
+// All three are bound by memory: one read of each input row and one write of each output row. A row
+// lives in the registers of one block (row.cuh), so x is read once although mean, variance (about the
+// mean, not from squares), the maximum for int8 and the output each need it; a block walks consecutive
+// rows with the weights of its columns in registers and the next row's loads in flight while it
+// reduces the present one.
+//
+// The gradient's column sums run in the same pass: a block adds its rows' dy xhat and dy into registers
+// (each thread its own columns: no atomics, a fixed order) and writes one slice of partial sums; a
+// second small kernel adds the slices of each group in order.
 #include "block.h"
+#include "common.cuh"
 #include "i8_quant.cuh"
-#include "types.cuh"
+#include "row.cuh"
 
 namespace svdq {
 namespace {
 
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[kThreads / 32];
+template <int E, int TEAM, int VEC>
+__device__ __forceinline__ void no_columns_beyond(float (&d)[E], int K) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
+  for (int i = 0; i < E; ++i)
+    if (row_column<TEAM, VEC>(i) >= K) d[i] = 0.0f;
+}
+
+// A tree of additions within the thread: the sum's longest chain stays short.
+template <int E>
+__device__ __forceinline__ float thread_sum(const float (&x)[E]) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += part[w];
-  return s;
+  for (int i = 0; i < E; ++i) s[i & 3] += x[i];
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+template <int E>
+__device__ __forceinline__ float thread_dot(const float (&x)[E], const float (&y)[E]) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < E; ++i) s[i & 3] = fmaf(x[i], y[i], s[i & 3]);
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-__device__ __forceinline__ float param(const void *p, int dtype, size_t i) {
-  if (dtype == SVDQ_F32) return static_cast<const float *>(p)[i];
-  if (dtype == SVDQ_F16) return to_f32(static_cast<const __half *>(p)[i]);
-  return to_f32(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
-
-struct RowStats {
-  float mean, rstd;
-};
-
-template <typename T>
-__device__ RowStats row_stats(const T *x, int K, float eps) {
-  float s = 0.0f;
-  for (int k = threadIdx.x; k < K; k += kThreads) s += to_f32(x[k]);
-  const float mean = block_sum(s) / K;
-  float q = 0.0f;
-  for (int k = threadIdx.x; k < K; k += kThreads) {
-    const float d = to_f32(x[k]) - mean;
-    q = fmaf(d, d, q);
+// Forward: rows [block's first, last) of X; QUANT writes int8 rows and their scales instead of Y.
+template <typename T, int TEAM, int E, int VEC, bool QUANT>
+__global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLaunch a, int rows_per_block) {
+  __shared__ BlockSum<TEAM, 1> sum;
+  __shared__ BlockMax<TEAM> top;
+  grid_dep_wait();
+  grid_dep_launch();
+  uint32_t turn = 0, tmax = 0;
+  const int m0 = blockIdx.x * rows_per_block;
+  const int m1 = min(a.M, m0 + rows_per_block);
+  const T *x0 = static_cast<const T *>(a.X);
+  RawRow<T, TEAM, VEC, E> next;
+  if (m0 < m1) next.load(x0 + m0 * a.x_stride, a.K);
+  float w[E], b[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    w[i] = 1.0f;
+    b[i] = 0.0f;
   }
-  return {mean, 1.0f / sqrtf(block_sum(q) / K + eps)};
-}
-
-__device__ __forceinline__ float affine(const NormLaunch &a, size_t g, int k, float xhat) {
-  const float w = a.weight ? a.weight_offset + param(a.weight, a.param_dtype, g * a.weight_stride + k) : 1.0f;
-  const float b = a.bias ? param(a.bias, a.param_dtype, g * a.bias_stride + k) : 0.0f;
-  return fmaf(xhat, w, b);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_layer_norm(NormLaunch a) {
-  const size_t m = blockIdx.x, g = m / a.rows_per_group;
-  const T *x = static_cast<const T *>(a.X) + m * a.x_stride;
-  const RowStats s = row_stats(x, a.K, a.eps);
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[m] = s.mean;
-    if (a.rstd) a.rstd[m] = s.rstd;
+  int group = -1;
+  const float inv_k = 1.0f / a.K;
+  for (int m = m0; m < m1; ++m) {
+    float x[E];
+    next.values(x);
+    if (m + 1 < m1) next.load(x0 + (m + 1) * a.x_stride, a.K);
+    if (m / a.rows_per_group != group) {
+      group = m / a.rows_per_group;
+      if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
+      if (a.bias) load_params<TEAM, VEC, E>(a.bias, a.param_dtype, group * a.bias_stride, a.K, 0.0f, b);
+    }
+    float v[1] = {thread_sum(x)};  // columns beyond K are zeros
+    sum(v, turn);
+    const float mean = v[0] * inv_k;
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] -= mean;
+    no_columns_beyond<E, TEAM, VEC>(x, a.K);
+    v[0] = thread_dot(x, x);
+    sum(v, turn);
+    const float rstd = 1.0f / sqrtf(fmaf(v[0], inv_k, a.eps));
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[m] = mean;
+      if (a.rstd) a.rstd[m] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = fmaf(x[i] * rstd, w[i], b[i]);
+    if constexpr (!QUANT) {
+      store_row<T, TEAM, VEC, E>(static_cast<T *>(a.Y) + m * a.y_stride, a.K, x);
+    } else {
+      no_columns_beyond<E, TEAM, VEC>(x, a.K);
+      uint32_t t = 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) t = max(t, abs_bits(x[i]));
+      const RowScale r = row_scale(top(t, tmax));
+      if (threadIdx.x == 0) a.x_scale[m] = r.scale;
+      int q[E];
+      i8_codes<E>(x, r, q);
+      store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, q);
+    }
   }
-  T *y = static_cast<T *>(a.Y) + m * a.y_stride;
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
-    y[k] = from_f32<T>(affine(a, g, k, (to_f32(x[k]) - s.mean) * s.rstd));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_layer_norm_quantize(NormLaunch a) {
-  const size_t m = blockIdx.x, g = m / a.rows_per_group;
-  const T *x = static_cast<const T *>(a.X) + m * a.x_stride;
-  const RowStats s = row_stats(x, a.K, a.eps);
-  uint32_t top = 0;
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
-    top = max(top, abs_bits(affine(a, g, k, (to_f32(x[k]) - s.mean) * s.rstd)));
-  const RowScale r = row_scale(block_max<kThreads>(top));
-  if (threadIdx.x == 0) a.x_scale[m] = r.scale;
-  int8_t *q = a.xq + m * a.K;
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
-    q[k] = i8_code(affine(a, g, k, (to_f32(x[k]) - s.mean) * s.rstd), r);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_layer_norm_dx(NormLaunch a) {
-  const size_t m = blockIdx.x, g = m / a.rows_per_group;
-  const T *x = static_cast<const T *>(a.X) + m * a.x_stride;
-  const T *dy = static_cast<const T *>(a.dY) + m * a.dy_stride;
-  T *dx = static_cast<T *>(a.dX) + m * a.dx_stride;
-  const float mean = a.mean[m], rstd = a.rstd[m];
-  auto gy = [&](int k) {
-    const float w = a.weight ? a.weight_offset + param(a.weight, a.param_dtype, g * a.weight_stride + k) : 1.0f;
-    return to_f32(dy[k]) * w;
-  };
-  float s0 = 0.0f, s1 = 0.0f;
-  for (int k = threadIdx.x; k < a.K; k += kThreads) {
-    const float v = gy(k);
-    s0 += v;
-    s1 = fmaf(v, (to_f32(x[k]) - mean) * rstd, s1);
+// Gradient: block (group g, slice s) takes rows [chunk s of the group]. Partial sums go to
+// partial[block][2][K], or straight to dweight and dbias where a group has one slice.
+template <typename T, int TEAM, int E, int VEC>
+__global__ void __launch_bounds__(TEAM, kBlocksPerSm<2 * TEAM>)
+    k_layer_norm_backward(NormLaunch a, int slices, int chunk) {
+  __shared__ BlockSum<TEAM, 2> sum;
+  grid_dep_launch();
+  uint32_t turn = 0;
+  const int group = blockIdx.x / slices, slice = blockIdx.x % slices;
+  const int64_t g0 = static_cast<int64_t>(group) * a.rows_per_group;
+  const int64_t g1 = g0 + a.rows_per_group < a.M ? g0 + a.rows_per_group : a.M;
+  const int64_t m0 = g0 + static_cast<int64_t>(slice) * chunk;
+  const int64_t m1 = m0 + chunk < g1 ? m0 + chunk : g1;
+  if (m0 >= m1) return;
+  const T *x0 = static_cast<const T *>(a.X), *dy0 = static_cast<const T *>(a.dY);
+  RawRow<T, TEAM, VEC, E> xn, dn;
+  xn.load(x0 + m0 * a.x_stride, a.K);
+  dn.load(dy0 + m0 * a.dy_stride, a.K);
+  float mean_n = a.mean[m0], rstd_n = a.rstd[m0];
+  float w[E], dw[E], db[E];
+  if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
+  const float inv_k = 1.0f / a.K;
+  for (int64_t m = m0; m < m1; ++m) {
+    float x[E], g[E];
+    xn.values(x);
+    dn.values(g);
+    const float mean = mean_n, rstd = rstd_n;
+    if (m + 1 < m1) {
+      xn.load(x0 + (m + 1) * a.x_stride, a.K);
+      dn.load(dy0 + (m + 1) * a.dy_stride, a.K);
+      mean_n = a.mean[m + 1];
+      rstd_n = a.rstd[m + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      x[i] = (x[i] - mean) * rstd;  // a column beyond K has g = 0
+      dw[i] = fmaf(g[i], x[i], dw[i]);
+      db[i] += g[i];
+      if (a.weight) g[i] *= w[i];
+    }
+    if (a.dX) {
+      float v[2] = {thread_sum(g), thread_dot(g, x)};
+      sum(v, turn);
+      const float c0 = v[0] * inv_k, c1 = v[1] * inv_k;
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = rstd * (g[i] - fmaf(x[i], c1, c0));
+      store_row<T, TEAM, VEC, E>(static_cast<T *>(a.dX) + m * a.dx_stride, a.K, x);
+    }
   }
-  const float m0 = block_sum(s0) / a.K, m1 = block_sum(s1) / a.K;
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
-    dx[k] = from_f32<T>(rstd * (gy(k) - m0 - (to_f32(x[k]) - mean) * rstd * m1));
+  if (!a.dweight && !a.dbias) return;
+  float *pw = slices == 1 ? a.dweight : a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.K;
+  float *pb = slices == 1 ? a.dbias : pw + a.K;
+  const size_t at = slices == 1 ? static_cast<size_t>(group) * a.K : 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int k = row_column<TEAM, VEC>(i);
+    if (k < a.K) {
+      if (pw) pw[at + k] = dw[i];
+      if (pb) pb[at + k] = db[i];
+    }
+  }
 }
 
-// One thread per column and group.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_layer_norm_dparam(NormLaunch a) {
-  const int k = blockIdx.x * kThreads + threadIdx.x;
-  if (k >= a.K) return;
-  const size_t g = blockIdx.y;
-  const size_t m0 = g * a.rows_per_group, m1 = min(static_cast<size_t>(a.M), m0 + a.rows_per_group);
+// dweight and dbias of (group, 32 columns) from the group's slices: eight warps add every eighth slice,
+// then their sums in order.
+__global__ void __launch_bounds__(256) k_layer_norm_slices(NormLaunch a, int slices, int chunk) {
+  __shared__ float part[2][8][32];
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k = blockIdx.x * 32 + lane;
+  const int group = blockIdx.y;
+  const int64_t g0 = static_cast<int64_t>(group) * a.rows_per_group;
+  const int64_t left = a.M - g0;
+  const int rows = left <= 0 ? 0 : static_cast<int>(left < a.rows_per_group ? left : a.rows_per_group);
+  const int n = (rows + chunk - 1) / chunk;  // slices that have rows
   float w = 0.0f, b = 0.0f;
-  for (size_t m = m0; m < m1; ++m) {
-    const float dy = to_f32(static_cast<const T *>(a.dY)[m * a.dy_stride + k]);
-    const float x = to_f32(static_cast<const T *>(a.X)[m * a.x_stride + k]);
-    w = fmaf(dy, (x - a.mean[m]) * a.rstd[m], w);
-    b += dy;
+  if (k < a.K) {
+    const float *p = a.partial + static_cast<size_t>(group) * slices * 2 * a.K + k;
+#pragma unroll 4
+    for (int s = warp; s < n; s += 8) {
+      w += p[static_cast<size_t>(s) * 2 * a.K];
+      b += p[static_cast<size_t>(s) * 2 * a.K + a.K];
+    }
   }
-  if (a.dweight) a.dweight[g * a.K + k] = w;
-  if (a.dbias) a.dbias[g * a.K + k] = b;
+  part[0][warp][lane] = w;
+  part[1][warp][lane] = b;
+  __syncthreads();
+  if (warp < 2 && k < a.K) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[warp][i][lane];
+    float *out = warp == 0 ? a.dweight : a.dbias;
+    if (out) out[static_cast<size_t>(group) * a.K + k] = s;
+  }
+}
+
+// Whether rows and parameters allow 16-byte vectors of T.
+template <typename T>
+bool vectors(const NormLaunch &a) {
+  constexpr size_t e = sizeof(T);
+  if (a.K % kVec<T>) return false;
+  const size_t pe = a.param_dtype == SVDQ_F32 ? 4 : 2;
+  const size_t pv = pe * kVec<T> < 16 ? pe * kVec<T> : 16;
+  auto rows = [&](const void *p, size_t stride) { return !p || rows_aligned(p, a.M > 1 ? stride : 0, e, 16); };
+  auto params = [&](const void *p, size_t stride) { return !p || rows_aligned(p, a.groups > 1 ? stride : 0, pe, pv); };
+  return rows(a.X, a.x_stride) && rows(a.Y, a.y_stride) && rows(a.dY, a.dy_stride) && rows(a.dX, a.dx_stride) &&
+         params(a.weight, a.weight_stride) && params(a.bias, a.bias_stride);
+}
+
+template <typename T, bool QUANT>
+cudaError_t forward_t(const NormLaunch &a) {
+  return for_row(a.K, [&]<int TEAM, int E>() {
+    // a block's rows are consecutive: as many blocks as are resident at once
+    const int blocks = a.num_sms * kBlocksPerSm<TEAM>;
+    const int rows = (a.M + blocks - 1) / blocks;
+    const dim3 grid((a.M + rows - 1) / rows);
+    if (vectors<T>(a)) return launch_dependent(k_layer_norm<T, TEAM, E, kVec<T>, QUANT>, grid, TEAM, 0, a.stream, a, rows);
+    return launch_dependent(k_layer_norm<T, TEAM, E, 1, QUANT>, grid, TEAM, 0, a.stream, a, rows);
+  });
+}
+
+template <bool QUANT>
+cudaError_t forward(const NormLaunch &a) {
+  if (a.dtype == SVDQ_F32) return forward_t<float, QUANT>(a);
+  if (a.dtype == SVDQ_F16) return forward_t<__half, QUANT>(a);
+  return forward_t<__nv_bfloat16, QUANT>(a);
+}
+
+// Slices of a group's rows in the backward pass and the rows of each: about two resident blocks of 512
+// threads for every SM over all groups, but no slice under four rows, whose partial sums would weigh
+// as much as the rows themselves.
+struct Slices {
+  int slices, chunk;
+};
+Slices slices_of(int M, int K, int rows_per_group) {
+  const int used = (M + rows_per_group - 1) / rows_per_group;
+  const int rows = M < rows_per_group ? M : rows_per_group;
+  const int team = for_row(K, []<int TEAM, int>() { return TEAM; });
+  const int blocks = 148 * (512 / team > 8 ? 8 : (512 / team < 1 ? 1 : 512 / team));
+  int s = blocks / used;
+  if (s > (rows + 3) / 4) s = (rows + 3) / 4;
+  if (s < 1) s = 1;
+  const int chunk = (rows + s - 1) / s;
+  return {(rows + chunk - 1) / chunk, chunk};
 }
 
 template <typename T>
 cudaError_t backward_t(const NormLaunch &a) {
-  // the sums first: dX may overwrite dY or X
-  if (a.dweight || a.dbias)
-    k_layer_norm_dparam<T><<<dim3((a.K + kThreads - 1) / kThreads, a.groups), kThreads, 0, a.stream>>>(a);
-  if (a.dX && a.M > 0) k_layer_norm_dx<T><<<a.M, kThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  const Slices s = slices_of(a.M, a.K, a.rows_per_group);
+  const int used = (a.M + a.rows_per_group - 1) / a.rows_per_group;
+  const bool sums = a.dweight || a.dbias;
+  if (sums && s.slices == 1 && used < a.groups) {
+    // groups behind the last row (the second kernel zeroes them where there is one)
+    const size_t at = static_cast<size_t>(used) * a.K, bytes = static_cast<size_t>(a.groups - used) * a.K * 4;
+    if (a.dweight && cudaMemsetAsync(a.dweight + at, 0, bytes, a.stream) != cudaSuccess) return cudaErrorUnknown;
+    if (a.dbias && cudaMemsetAsync(a.dbias + at, 0, bytes, a.stream) != cudaSuccess) return cudaErrorUnknown;
+  }
+  const cudaError_t e = for_row(a.K, [&]<int TEAM, int E>() {
+    const dim3 grid(static_cast<unsigned>(used) * s.slices);
+    if (vectors<T>(a)) k_layer_norm_backward<T, TEAM, E, kVec<T>><<<grid, TEAM, 0, a.stream>>>(a, s.slices, s.chunk);
+    else k_layer_norm_backward<T, TEAM, E, 1><<<grid, TEAM, 0, a.stream>>>(a, s.slices, s.chunk);
+    return cudaGetLastError();
+  });
+  if (e != cudaSuccess || !sums || s.slices == 1) return e;
+  return launch_dependent(k_layer_norm_slices, dim3((a.K + 31) / 32, a.groups), 256, 0, a.stream, a, s.slices, s.chunk);
 }
 
 }  // namespace
 
-cudaError_t launch_layer_norm(const NormLaunch &a) {
-  if (a.dtype == SVDQ_F32) k_layer_norm<float><<<a.M, kThreads, 0, a.stream>>>(a);
-  else if (a.dtype == SVDQ_F16) k_layer_norm<__half><<<a.M, kThreads, 0, a.stream>>>(a);
-  else k_layer_norm<__nv_bfloat16><<<a.M, kThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
-}
+cudaError_t launch_layer_norm(const NormLaunch &a) { return forward<false>(a); }
 
-cudaError_t launch_layer_norm_quantize(const NormLaunch &a) {
-  if (a.dtype == SVDQ_F32) k_layer_norm_quantize<float><<<a.M, kThreads, 0, a.stream>>>(a);
-  else if (a.dtype == SVDQ_F16) k_layer_norm_quantize<__half><<<a.M, kThreads, 0, a.stream>>>(a);
-  else k_layer_norm_quantize<__nv_bfloat16><<<a.M, kThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
-}
+cudaError_t launch_layer_norm_quantize(const NormLaunch &a) { return forward<true>(a); }
 
-size_t layer_norm_partial_bytes(int, int, int, int) { return 0; }
+size_t layer_norm_partial_bytes(int M, int K, int groups, int rows_per_group) {
+  const Slices s = slices_of(M, K, rows_per_group);
+  if (s.slices == 1) return 0;
+  const size_t used = (static_cast<size_t>(M) + rows_per_group - 1) / rows_per_group;
+  (void)groups;
+  return (used * s.slices * 2 * K * sizeof(float) + 15) / 16 * 16;
+}
 
 cudaError_t launch_layer_norm_backward(const NormLaunch &a) {
   if (a.dtype == SVDQ_F32) return backward_t<float>(a);

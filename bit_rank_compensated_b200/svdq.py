@@ -509,14 +509,13 @@ def unfused_forward(X, layer, bufs, Y, stream=None):
 
 # ---------------------------------------------------------------- operators around the projections
 # Unlike the calls above these check what they are given (shapes, types, devices; ValueError), since
-# their rows may be strided views, and run on the tensors' device whichever is current.
+# their rows may be strided views, and run on the tensors' device whichever is current. A call costs a
+# few microseconds of the host's time, which is what small ones take: messages are only made on failure.
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3, torch.int64: 4}
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
-
-
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
+_INT8 = (torch.int8,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(name: str, device: torch.device, *args):
@@ -524,33 +523,12 @@ def _run(name: str, device: torch.device, *args):
     index = device.index
     fn = getattr(_lib or load(), name)
     if index == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, _raw_stream(index))
     if status != SVDQ_OK:
         _check(name, status)
-
-
-def _rows(t, name: str, dtypes=_FLOATS):
-    """(rows, columns, row stride) of a matrix whose rows are contiguous."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.dim() == 2, f"{name} must have two dimensions, got {t.dim()}")
-    _need(t.dtype in dtypes, f"{name} has the unsupported type {t.dtype}")
-    M, K = t.shape
-    _need(K <= 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
-    stride = t.stride(0) if M > 1 else K
-    _need(stride >= K, f"the rows of {name} overlap")
-    return M, K, stride
-
-
-def _vector(t, name: str, n: int, device, dtype=torch.float32):
-    """A contiguous vector of n values (or None); its address."""
-    if t is None:
-        return None
-    _need(isinstance(t, torch.Tensor) and t.device == device, f"{name} must be on {device}")
-    _need(t.dtype == dtype and t.numel() == n and t.is_contiguous(), f"{name} must be {n} contiguous {dtype} values")
-    return t.data_ptr()
 
 
 def _on_stream(stream, fn, *args, **kw):
@@ -559,36 +537,72 @@ def _on_stream(stream, fn, *args, **kw):
         return fn(*args, **kw)
 
 
-def _norm_affine(X, M: int, K: int, weight, bias, rows_per_group, weight_offset: float):
-    """The C struct of a layer norm's weight and bias ([K] or [groups, K]), and the number of groups."""
-    groups, dtype = 1, torch.float32
-    s = NormAffineStruct()
-    for name, t in (("weight", weight), ("bias", bias)):
+def _rows(t, name: str, dtypes=_FLOATS):
+    """(rows, columns, row stride) of a matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a two-dimensional CUDA tensor of {', '.join(map(str, dtypes))}")
+    M, K = t.shape
+    stride, one = t.stride()
+    if M <= 1:
+        stride = K
+    if (one != 1 and K > 1) or stride < K:
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    return M, K, stride
+
+
+def _vector(t, name: str, n: int, device, dtype=torch.float32):
+    """Address of n contiguous values (of a vector or matrix), or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype} values on {device}")
+    return t.data_ptr()
+
+
+def _like(out, X, M: int, K: int, name: str):
+    """A caller's output of X's type, checked, or a new one; and its row stride."""
+    if out is None:
+        return X.new_empty((M, K)), K
+    m, k, stride = _rows(out, name, (X.dtype,))
+    if (m, k) != (M, K) or out.device != X.device:
+        raise ValueError(f"{name} must be {M} x {K} on {X.device}")
+    return out, stride
+
+
+def _workspace(t, size: int, device):
+    """(address, bytes) of a caller's workspace, or of a new one of `size` bytes, and what keeps it alive."""
+    if t is None:
+        if not size:
+            return None, 0, None
+        t = torch.empty(size, dtype=torch.uint8, device=device)
+    elif t.device != device or not t.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {device}")
+    return t.data_ptr(), t.numel() * t.element_size(), t
+
+
+def _norm_affine(X, M: int, K: int, weight, bias, rows_per_group: int, weight_offset: float, groups: int | None = None):
+    """The C struct of a layer norm's weight and bias ([K] or [groups, K])."""
+    w = b = None
+    w_stride = b_stride = 0
+    n, dtype = groups, torch.float32
+    for i, t in enumerate((weight, bias)):
         if t is None:
             continue
-        t = t[None] if t.dim() == 1 else t
-        n, k, stride = _rows(t, name)
-        _need(k == K and t.device == X.device, f"{name} must have {K} columns and be on {X.device}")
-        other = bias if name == "weight" else weight
-        _need(other is None or (other.dtype == t.dtype and other.numel() == t.numel()),
-              "weight and bias must have one type and shape")
-        groups, dtype = n, t.dtype
-        setattr(s, name, t.data_ptr())
-        setattr(s, name + "_stride", stride)
-    rows = rows_per_group or max(1, -(-M // max(1, groups)))
-    _need(groups >= 1 and rows >= 1 and groups * rows >= M, f"{groups} groups of {rows} rows do not cover {M} rows")
-    s.dtype, s.groups, s.rows_per_group, s.weight_offset = DTYPES[dtype], groups, rows, weight_offset
-    return s, groups
-
-
-def _like(out, X, shape, dtype, name: str):
-    """A caller's output, checked, or a new one; and its row stride."""
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=X.device)
-        return out, shape[1]
-    M, K, stride = _rows(out, name, (dtype,))
-    _need((M, K) == tuple(shape) and out.device == X.device, f"{name} must be {tuple(shape)} on {X.device}")
-    return out, stride
+        name = "bias" if i else "weight"
+        g, k, stride = _rows(t if t.dim() == 2 else t[None], name)
+        if k != K or t.device != X.device or (n is not None and g != n) or (w is not None and t.dtype != dtype):
+            raise ValueError(f"weight and bias must be of one type and shape, with {K} columns, on {X.device}")
+        n, dtype = g, t.dtype
+        if i:
+            b, b_stride = t.data_ptr(), stride
+        else:
+            w, w_stride = t.data_ptr(), stride
+    if n is None:
+        n = 1
+    rows = rows_per_group or max(1, -(-M // max(n, 1)))
+    if n < 1 or rows < 1 or n * rows < M:
+        raise ValueError(f"{n} groups of {rows} rows do not cover {M} rows")
+    return NormAffineStruct(w, b, w_stride, b_stride, DTYPES[dtype], n, rows, weight_offset)
 
 
 def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset: float = 0.0, eps: float = 1e-6,
@@ -601,10 +615,11 @@ def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset
     if stream is not None:
         return _on_stream(stream, layer_norm, X, weight, bias, rows_per_group, weight_offset, eps, Y, stats)
     M, K, x_stride = _rows(X, "X")
-    affine, _ = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
-    Y, y_stride = _like(Y, X, (M, K), X.dtype, "Y")
-    mean = torch.empty(M, dtype=torch.float32, device=X.device) if stats else None
-    rstd = torch.empty(M, dtype=torch.float32, device=X.device) if stats else None
+    affine = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
+    Y, y_stride = _like(Y, X, M, K, "Y")
+    mean = rstd = None
+    if stats:
+        mean, rstd = X.new_empty((2, M), dtype=torch.float32).unbind(0)
     _run("svdq_layer_norm", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K, ctypes.addressof(affine), eps,
          Y.data_ptr(), y_stride, mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None)
     return (Y, mean, rstd) if stats else Y
@@ -621,35 +636,37 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0,
                           groups, need_dX, need_dweight, need_dbias, workspace)
     M, K, x_stride = _rows(X, "X")
     m, k, dy_stride = _rows(dY, "dY", (X.dtype,))
-    _need((m, k) == (M, K) and dY.device == X.device, "dY must have X's shape and device")
-    affine, n = _norm_affine(X, M, K, weight, None, rows_per_group, weight_offset)
-    if weight is None and groups:
-        n = affine.groups = groups
-        affine.rows_per_group = rows_per_group or max(1, -(-M // groups))
-        _need(groups >= 1 and affine.rows_per_group * groups >= M, f"the groups do not cover {M} rows")
-    _need(groups is None or groups == n, "groups must be the weight's number of rows")
-    dx_stride = K
+    device = X.device
+    if m != M or k != K or dY.device != device:
+        raise ValueError(f"dY must be {M} x {K} on {device}")
+    affine = _norm_affine(X, M, K, weight, None, rows_per_group, weight_offset, groups)
+    dx_stride, dx, dw, db, sums = K, None, None, None, None
     if need_dX:
-        dX, dx_stride = _like(dX, X, (M, K), X.dtype, "dX")
+        dX, dx_stride = _like(dX, X, M, K, "dX")
+        dx = dX.data_ptr()
     else:
         dX = None
-    dw = torch.empty(n, K, dtype=torch.float32, device=X.device) if need_dweight else None
-    db = torch.empty(n, K, dtype=torch.float32, device=X.device) if need_dbias else None
-    size = load().svdq_layer_norm_workspace_bytes(M, K, n, affine.rows_per_group) if dw is not None or db is not None else 0
-    if size and workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=X.device)
-    _run("svdq_layer_norm_backward", X.device, dY.data_ptr(), dy_stride, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
-         ctypes.addressof(affine), _vector(mean, "mean", M, X.device), _vector(rstd, "rstd", M, X.device),
-         None if dX is None else dX.data_ptr(), dx_stride, None if dw is None else dw.data_ptr(),
-         None if db is None else db.data_ptr(), *_workspace(workspace, X.device))
+    n = affine.groups
+    if need_dweight or need_dbias:
+        sums = X.new_empty((need_dweight + need_dbias, n, K), dtype=torch.float32)
+        dw = sums[0] if need_dweight else None
+        db = sums[-1] if need_dbias else None
+    size = load().svdq_layer_norm_workspace_bytes(M, K, n, affine.rows_per_group) if sums is not None else 0
+    space, size, kept = _workspace(workspace, size, device)
+    _run("svdq_layer_norm_backward", device, dY.data_ptr(), dy_stride, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+         ctypes.addressof(affine), _vector(mean, "mean", M, device), _vector(rstd, "rstd", M, device), dx, dx_stride,
+         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), space, size)
     return dX, dw, db
 
 
-def _workspace(t, device):
-    if t is None:
-        return None, 0
-    _need(t.device == device and t.is_contiguous(), f"the workspace must be contiguous and on {device}")
-    return t.data_ptr(), t.numel() * t.element_size()
+def _i8_rows(X, M: int, K: int, xq, x_scale):
+    """Int8 rows and scales: the caller's, checked, or new ones; and their addresses."""
+    device = X.device
+    if xq is None:
+        xq = X.new_empty((M, K), dtype=torch.int8)
+    if x_scale is None:
+        x_scale = X.new_empty(M, dtype=torch.float32)
+    return xq, x_scale, _vector(xq, "xq", M * K, device, torch.int8), _vector(x_scale, "x_scale", M, device)
 
 
 def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
@@ -658,21 +675,9 @@ def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
     if stream is not None:
         return _on_stream(stream, i8_quantize_rows, X, col_scale, xq, x_scale)
     M, K, x_stride = _rows(X, "X")
-    xq, x_scale = _i8_rows(X, M, K, xq, x_scale)
+    xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
     _run("svdq_i8_quantize_rows", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
-         _vector(col_scale, "col_scale", K, X.device), xq.data_ptr(), x_scale.data_ptr())
-    return xq, x_scale
-
-
-def _i8_rows(X, M: int, K: int, xq, x_scale):
-    if xq is None:
-        xq = torch.empty(M, K, dtype=torch.int8, device=X.device)
-    else:
-        _vector(xq, "xq", M * K, X.device, torch.int8)
-    if x_scale is None:
-        x_scale = torch.empty(M, dtype=torch.float32, device=X.device)
-    else:
-        _vector(x_scale, "x_scale", M, X.device)
+         _vector(col_scale, "col_scale", K, X.device), q, s)
     return xq, x_scale
 
 
@@ -683,10 +688,10 @@ def i8_layer_norm_quantize(X, weight=None, bias=None, rows_per_group: int = 0, w
         return _on_stream(stream, i8_layer_norm_quantize, X, weight, bias, rows_per_group, weight_offset, eps, xq,
                           x_scale)
     M, K, x_stride = _rows(X, "X")
-    affine, _ = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
-    xq, x_scale = _i8_rows(X, M, K, xq, x_scale)
+    affine = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
+    xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
     _run("svdq_i8_layer_norm_quantize", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
-         ctypes.addressof(affine), eps, xq.data_ptr(), x_scale.data_ptr())
+         ctypes.addressof(affine), eps, q, s)
     return xq, x_scale
 
 
@@ -695,33 +700,28 @@ def i8_workspace_bytes(M: int, N: int, K: int) -> int:
 
 
 def _i8_weight(wq, w_scale, bias, K: int, device):
-    _need(isinstance(wq, torch.Tensor) and wq.dim() == 2 and wq.shape[1] == K, f"wq must have {K} columns")
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2 or wq.shape[1] != K:
+        raise ValueError(f"wq must be a matrix of {K} columns")
     N = wq.shape[0]
-    return N, (_vector(wq, "wq", N * K, device, torch.int8), _vector(w_scale, "w_scale", N, device),
-               _vector(bias, "bias", N, device))
-
-
-def _i8_output(Y, workspace, M: int, N: int, K: int, dtype, device):
-    if Y is None:
-        Y = torch.empty(M, N, dtype=dtype, device=device)
-    else:
-        _vector(Y, "Y", M * N, device, dtype)
-    size = load().svdq_i8_workspace_bytes(M, N, K)
-    if size and workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    return Y, _workspace(workspace, device)
+    return (N, _vector(wq, "wq", N * K, device, torch.int8), _vector(w_scale, "w_scale", N, device),
+            _vector(bias, "bias", N, device))
 
 
 def i8_gemm(xq, x_scale, wq, w_scale, bias=None, Y=None, dtype=torch.bfloat16, workspace=None, stream=None):
     """Y [M, N] = (xq wq^T) * x_scale[:, None] * w_scale + bias from int8 rows, with exact integer sums."""
     if stream is not None:
         return _on_stream(stream, i8_gemm, xq, x_scale, wq, w_scale, bias, Y, dtype, workspace)
-    M, K, _ = _rows(xq, "xq", (torch.int8,))
-    _need(xq.is_contiguous() and dtype in _FLOATS, "xq must be contiguous, and dtype a floating type of 16 or 32 bits")
-    N, (w, ws, b) = _i8_weight(wq, w_scale, bias, K, xq.device)
-    Y, space = _i8_output(Y, workspace, M, N, K, dtype, xq.device)
-    _run("svdq_i8_gemm", xq.device, xq.data_ptr(), _vector(x_scale, "x_scale", M, xq.device), M, w, ws, b, N, K,
-         Y.data_ptr(), DTYPES[dtype], *space)
+    M, K, _ = _rows(xq, "xq", _INT8)
+    device = xq.device
+    if dtype not in _FLOATS:
+        raise ValueError(f"dtype must be one of {_FLOATS}")
+    N, w, ws, b = _i8_weight(wq, w_scale, bias, K, device)
+    x, xs = _vector(xq, "xq", M * K, device, torch.int8), _vector(x_scale, "x_scale", M, device)
+    if Y is None:
+        Y = xq.new_empty((M, N), dtype=dtype)
+    y = _vector(Y, "Y", M * N, device, dtype)
+    space, size, kept = _workspace(workspace, load().svdq_i8_workspace_bytes(M, N, K), device)
+    _run("svdq_i8_gemm", device, x, xs, M, w, ws, b, N, K, y, DTYPES[dtype], space, size)
     return Y
 
 
@@ -732,12 +732,15 @@ def i8_linear_forward(X, wq, w_scale, bias=None, col_scale=None, xq=None, x_scal
     if stream is not None:
         return _on_stream(stream, i8_linear_forward, X, wq, w_scale, bias, col_scale, xq, x_scale, Y, workspace)
     M, K, x_stride = _rows(X, "X")
-    N, (w, ws, b) = _i8_weight(wq, w_scale, bias, K, X.device)
-    xq, x_scale = _i8_rows(X, M, K, xq, x_scale)
-    Y, space = _i8_output(Y, workspace, M, N, K, X.dtype, X.device)
-    _run("svdq_i8_linear_forward", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M,
-         _vector(col_scale, "col_scale", K, X.device), w, ws, b, N, K, xq.data_ptr(), x_scale.data_ptr(), Y.data_ptr(),
-         *space)
+    device = X.device
+    N, w, ws, b = _i8_weight(wq, w_scale, bias, K, device)
+    xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
+    if Y is None:
+        Y = X.new_empty((M, N))
+    y = _vector(Y, "Y", M * N, device, X.dtype)
+    space, size, kept = _workspace(workspace, load().svdq_i8_workspace_bytes(M, N, K), device)
+    _run("svdq_i8_linear_forward", device, X.data_ptr(), x_stride, DTYPES[X.dtype], M,
+         _vector(col_scale, "col_scale", K, device), w, ws, b, N, K, q, s, y, space, size)
     return Y
 
 
@@ -749,19 +752,24 @@ class RopeAxes:
     Pair p is columns (2p, 2p + 1), or with halves (p, p + sum(pairs))."""
 
     def __init__(self, pairs, theta: float = 10000.0, shared_ladder: bool = False, halves: bool = False):
-        _need(1 <= len(pairs) <= 4 and min(pairs) >= 1, "one to four axes of at least one pair are supported")
+        if not 1 <= len(pairs) <= 4 or min(pairs) < 1:
+            raise ValueError("one to four axes of at least one pair are supported")
         self.pairs, self.theta = tuple(pairs), float(theta)
         self.n_pairs = sum(pairs)
-        self.s = RopeAxesStruct(len(pairs), tuple(pairs), int(shared_ladder), int(halves), theta)
+        self.s = RopeAxesStruct(len(pairs), self.pairs, bool(shared_ladder), bool(halves), self.theta)
+        self.address = ctypes.addressof(self.s)
 
 
-def _positions(pos, axes: RopeAxes):
-    _need(isinstance(pos, torch.Tensor) and pos.is_cuda and pos.dtype in (torch.int32, torch.int64, torch.float32),
-          "pos must be a CUDA tensor of int32, int64 or fp32")
+def _positions(pos, axes: RopeAxes, M=None, device=None):
+    if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype not in (torch.int64, torch.int32, torch.float32):
+        raise ValueError("pos must be a CUDA tensor of int32, int64 or fp32")
     if pos.dim() == 1:
         pos = pos[:, None]
-    _need(pos.dim() == 2 and pos.shape[1] == len(axes.pairs), f"pos must be [tokens, {len(axes.pairs)}]")
-    return PositionsStruct(pos.data_ptr(), DTYPES[pos.dtype], pos.stride(0), pos.stride(1))
+    if (pos.dim() != 2 or pos.shape[1] != len(axes.pairs) or (M is not None and pos.shape[0] != M)
+            or (device is not None and pos.device != device)):
+        raise ValueError(f"pos must be [tokens, {len(axes.pairs)}], with the heads' tokens and device")
+    token, axis = pos.stride()
+    return PositionsStruct(pos.data_ptr(), DTYPES[pos.dtype], token, axis)
 
 
 def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
@@ -772,25 +780,31 @@ def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
     p = _positions(pos, axes)
     M, n = pos.shape[0], axes.n_pairs
     if table is None:
-        table = torch.empty(M, n, 2, dtype=torch.float32, device=pos.device)
-    _run("svdq_rope_axes_table", pos.device, ctypes.addressof(p), M, ctypes.addressof(axes.s),
+        table = pos.new_empty((M, n, 2), dtype=torch.float32)
+    _run("svdq_rope_axes_table", pos.device, ctypes.addressof(p), M, axes.address,
          _vector(table, "table", 2 * M * n, pos.device))
     return table
 
 
 def _heads(t, out, name: str, like):
     """The C structs of heads [M, H, D] and of their output (a new one unless given)."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3, f"{name} must be a CUDA tensor [tokens, heads, columns]")
-    _need(t.dtype in _FLOATS and t.dtype == like.dtype and t.device == like.device and t.shape[0] == like.shape[0]
-          and t.shape[2] == like.shape[2], f"{name}'s type, device, tokens or columns differ from what they must be")
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype not in _FLOATS
+            or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be [tokens, heads, columns] on a GPU, of one floating type and device with q")
+    M, H, D = t.shape
+    if M != like.shape[0] or D != like.shape[2]:
+        raise ValueError(f"{name} must have q's tokens and columns")
+    token, head, one = t.stride()
     if out is None:
-        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    _need(out.shape == t.shape and out.dtype == t.dtype and out.device == t.device, f"{name}_out must be like {name}")
-    s = []
-    for v in (t, out):
-        _need(v.stride(2) == 1, f"the columns of {name} must be contiguous")
-        s.append(HeadsStruct(v.data_ptr(), v.shape[1], v.stride(0), v.stride(1)))
-    return s[0], s[1], out
+        out = t.new_empty((M, H, D))
+        to = (H * D, D, 1)
+    else:
+        if out.shape != t.shape or out.dtype != t.dtype or out.device != t.device:
+            raise ValueError(f"{name}_out must be like {name}")
+        to = out.stride()
+    if one != 1 or to[2] != 1:
+        raise ValueError(f"the columns of {name} and its output must be contiguous")
+    return HeadsStruct(t.data_ptr(), H, token, head), HeadsStruct(out.data_ptr(), H, to[0], to[1]), out
 
 
 def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -799,16 +813,18 @@ def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None
     be q and k. Returns (q_out, k_out)."""
     if stream is not None:
         return _on_stream(stream, rope_axes_apply, q, k, pos, axes, inverse, q_out, k_out)
+    at = ctypes.addressof
     qi, qo, q_out = _heads(q, q_out, "q", q)
     ki = ko = None
     if k is not None:
         ki, ko, k_out = _heads(k, k_out, "k", q)
-    p = _positions(pos, axes)
-    _need(pos.shape[0] == q.shape[0] and pos.device == q.device, "pos must have q's tokens and device")
-    at = ctypes.addressof
-    _run("svdq_rope_axes_apply", q.device, at(qi), at(qo), None if k is None else at(ki), None if k is None else at(ko),
-         DTYPES[q.dtype], q.shape[0], q.shape[2], at(p), at(axes.s), int(inverse))
-    return q_out, (None if k is None else k_out)
+    else:
+        k_out = None
+    M, _, D = q.shape
+    p = _positions(pos, axes, M, q.device)
+    _run("svdq_rope_axes_apply", q.device, at(qi), at(qo), ki and at(ki), ko and at(ko), DTYPES[q.dtype], M, D, at(p),
+         axes.address, bool(inverse))
+    return q_out, k_out
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:

@@ -308,7 +308,8 @@ SVDQ_API svdq_status svdq_awq_gemv_w4a16(const uint16_t *X, int M, const uint8_t
  * Pointers of these calls are device pointers aligned to their element (16 bytes where stated;
  * SVDQ_ERR_MISALIGNED otherwise); rows need not be contiguous: a stride is the distance of two
  * rows in elements. An output may be an input's own buffer (same address and strides) where
- * stated; otherwise buffers do not overlap. */
+ * stated; otherwise buffers do not overlap. M (rows, tokens) is at most 2^30; with M = 0 there is
+ * nothing to do, and pointers to rows may be NULL. */
 typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_F16 = 1, SVDQ_F32 = 2, SVDQ_I32 = 3, SVDQ_I64 = 4 } svdq_dtype;
 
 /* Weight and bias of a layer norm, one row of K values for each group of consecutive rows of X
@@ -330,7 +331,7 @@ typedef struct svdq_norm_affine {
  *   X, Y    device, M x K of dtype (Y may be X).
  *   affine  host struct, or NULL for Y = xhat.
  *   mean, rstd  device, M fp32 each, or NULL (kept for the backward pass).
- * 1 <= K <= 16384, M >= 0 (0: nothing to do), strides >= K, eps >= 0. Asynchronous on stream. */
+ * 1 <= K <= 16384, strides >= K, eps >= 0 and finite. Asynchronous on stream. */
 SVDQ_API svdq_status svdq_layer_norm(const void *X, size_t x_stride, int dtype, int M, int K,
                                      const svdq_norm_affine *affine, float eps, void *Y, size_t y_stride,
                                      float *mean, float *rstd, void *stream);
@@ -374,7 +375,7 @@ SVDQ_API svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, 
  *                then NULL is fine): partial sums where few tokens leave the K axis to be split.
  * svdq_i8_linear_forward: svdq_i8_quantize_rows, then svdq_i8_gemm with Y of X's dtype; xq and
  *     x_scale are scratch of the sizes above.
- * M >= 0 (0: nothing to do). Asynchronous on stream. */
+ * Asynchronous on stream. */
 SVDQ_API svdq_status svdq_i8_quantize_rows(const void *X, size_t x_stride, int dtype, int M, int K,
                                            const float *col_scale, int8_t *xq, float *x_scale, void *stream);
 SVDQ_API svdq_status svdq_i8_layer_norm_quantize(const void *X, size_t x_stride, int dtype, int M, int K,
@@ -428,7 +429,7 @@ SVDQ_API svdq_status svdq_rope_axes_table(const svdq_positions *pos, int M, cons
  *   which undoes the rotation and is its gradient. Columns from 2 P on are copied.
  *   q, k        inputs (k NULL: Q alone), of dtype; heads and strides may differ (shared K heads).
  *   q_out, k_out  outputs, the same number of heads; may be the inputs themselves (same strides).
- * head_dim even, 2 P <= head_dim <= 512; at most 65536 heads; strides >= head_dim; M >= 0. Asynchronous on stream. */
+ * head_dim even, 2 P <= head_dim <= 512; at most 65536 heads; strides >= head_dim. Asynchronous on stream. */
 SVDQ_API svdq_status svdq_rope_axes_apply(const svdq_heads *q, const svdq_heads *q_out, const svdq_heads *k,
                                           const svdq_heads *k_out, int dtype, int M, int head_dim,
                                           const svdq_positions *pos, const svdq_rope_axes *axes, int inverse,

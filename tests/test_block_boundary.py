@@ -128,12 +128,12 @@ INVALID_ARGS = [
     *[(c, dict(K=131088, xs=131088)) for c in ("_quantize", "_gemm", "_linear")],
     *[(c, dict(K=56)) for c in ("_quantize", "_norm_quantize", "_gemm", "_linear")],
     *[(c, dict(N=n)) for c in ("_gemm", "_linear") for n in (0, -16, 24)],
-    *[(c, {p: None}) for c, ps in (("_norm", ["Y"]), ("_backward", ["dY", "mean", "rstd"]), ("_quantize", ["xq", "s"]),
+    *[(c, {p: None}) for c, ps in (("_norm", ["Y"]), ("_backward", ["dY", "mean", "rstd", "ws"]), ("_quantize", ["xq", "s"]),
                                   ("_norm_quantize", ["xq", "s"]), ("_gemm", ["xq", "s", "wq", "ws", "Y"]),
                                   ("_linear", ["xq", "s", "wq", "ws", "Y"]), ("_table", ["pos", "axes", "table"]),
                                   ("_apply", ["q", "qo", "k", "ko", "pos", "axes"])) for p in ps],
     ("_norm", dict(ys=63)), ("_norm", dict(eps=-1e-6)), ("_norm", dict(eps=float("nan"))), ("_norm_quantize", dict(eps=float("inf"))),
-    ("_backward", dict(dys=63)), ("_backward", dict(dxs=63)),
+    ("_backward", dict(dys=63)), ("_backward", dict(dxs=63)), ("_backward", dict(wsb=16)),
     *[(c, dict(af=a)) for c in ("_norm", "_backward", "_norm_quantize") for a in ("dtype=3", "groups=0", "groups=1", "rows_per_group=0",
                                                                                 "rows_per_group=49", "weight_stride=63", "bias_stride=0")],
     *[(c, dict(axes=a)) for c in ("_table", "_apply") for a in ("n_axes=0", "n_axes=5", "pairs=(0,8,0,0)", "pairs=(200,200,0,0)",
