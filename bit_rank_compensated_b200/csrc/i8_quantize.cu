@@ -3,7 +3,6 @@
 // writes its codes; a longer one is read a second time, from L2.
 #include "block.h"
 #include "common.cuh"
-#include "i8_quant.cuh"
 #include "row.cuh"
 
 namespace svdq {
@@ -15,28 +14,22 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_quantize_rows(Quan
   grid_dep_wait();
   grid_dep_launch();
   uint32_t turn = 0;
-  const int m0 = blockIdx.x * rows_per_block;
-  const int m1 = min(a.M, m0 + rows_per_block);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
+  const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  RawRow<T, TEAM, VEC, E> next;
-  if (m0 < m1) next.load(x0 + m0 * a.x_stride, a.K);
-  float c[E];
-  if (a.col_scale) load_params<TEAM, VEC, E>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
-  for (int m = m0; m < m1; ++m) {
+  RowsAhead<T, TEAM, VEC, E> ahead;
+  ahead.start(x0, a.x_stride, m0, m1, a.K);
+  for (int64_t m = m0; m < m1; ++m) {
     float x[E];
-    next.values(x);
-    if (m + 1 < m1) next.load(x0 + (m + 1) * a.x_stride, a.K);
+    ahead.take(x0, a.x_stride, m, m1, a.K, x);
+    if (a.col_scale)
+      with_params<TEAM, VEC, E>(a.col_scale, SVDQ_F32, 0, a.K, [&](int i, float c) { x[i] = __fmul_rn(x[i], c); });
     uint32_t t = 0;  // columns beyond K are zeros
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if (a.col_scale) x[i] = __fmul_rn(x[i], c[i]);
-      t = max(t, abs_bits(x[i]));
-    }
+    for (int i = 0; i < E; ++i) t = max(t, abs_bits(x[i]));
     const RowScale r = row_scale(top(t, turn));
     if (threadIdx.x == 0) a.x_scale[m] = r.scale;
-    int q[E];
-    i8_codes<E>(x, r, q);
-    store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, q);
+    store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
   }
 }
 

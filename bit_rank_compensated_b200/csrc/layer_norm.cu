@@ -6,15 +6,13 @@
 // All three are bound by memory: one read of each input row and one write of each output row. A row
 // lives in the registers of one block (row.cuh), so x is read once although mean, variance (about the
 // mean, not from squares), the maximum for int8 and the output each need it; a block walks consecutive
-// rows with the weights of its columns in registers and the next row's loads in flight while it
-// reduces the present one.
+// rows with the next rows' loads in flight while it reduces the present one, and finds weights in L1.
 //
 // The gradient's column sums run in the same pass: a block adds its rows' dy xhat and dy into registers
 // (each thread its own columns: no atomics, a fixed order) and writes one slice of partial sums; a
 // second small kernel adds the slices of each group in order.
 #include "block.h"
 #include "common.cuh"
-#include "i8_quant.cuh"
 #include "row.cuh"
 
 namespace svdq {
@@ -51,28 +49,16 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLau
   grid_dep_wait();
   grid_dep_launch();
   uint32_t turn = 0, tmax = 0;
-  const int m0 = blockIdx.x * rows_per_block;
-  const int m1 = min(a.M, m0 + rows_per_block);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
+  const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  RawRow<T, TEAM, VEC, E> next;
-  if (m0 < m1) next.load(x0 + m0 * a.x_stride, a.K);
-  float w[E], b[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    w[i] = 1.0f;
-    b[i] = 0.0f;
-  }
-  int group = -1;
+  RowsAhead<T, TEAM, VEC, E> ahead;
+  ahead.start(x0, a.x_stride, m0, m1, a.K);
   const float inv_k = 1.0f / a.K;
-  for (int m = m0; m < m1; ++m) {
+  for (int64_t m = m0; m < m1; ++m) {
     float x[E];
-    next.values(x);
-    if (m + 1 < m1) next.load(x0 + (m + 1) * a.x_stride, a.K);
-    if (m / a.rows_per_group != group) {
-      group = m / a.rows_per_group;
-      if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
-      if (a.bias) load_params<TEAM, VEC, E>(a.bias, a.param_dtype, group * a.bias_stride, a.K, 0.0f, b);
-    }
+    ahead.take(x0, a.x_stride, m, m1, a.K, x);
+    const size_t group = static_cast<int>(m) / a.rows_per_group;
     float v[1] = {thread_sum(x)};  // columns beyond K are zeros
     sum(v, turn);
     const float mean = v[0] * inv_k;
@@ -87,19 +73,21 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLau
       if (a.rstd) a.rstd[m] = rstd;
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = fmaf(x[i] * rstd, w[i], b[i]);
+    for (int i = 0; i < E; ++i) x[i] *= rstd;
+    if (a.weight)
+      with_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K,
+                                [&](int i, float w) { x[i] *= a.weight_offset + w; });
+    if (a.bias)
+      with_params<TEAM, VEC, E>(a.bias, a.param_dtype, group * a.bias_stride, a.K, [&](int i, float b) { x[i] += b; });
     if constexpr (!QUANT) {
       store_row<T, TEAM, VEC, E>(static_cast<T *>(a.Y) + m * a.y_stride, a.K, x);
     } else {
-      no_columns_beyond<E, TEAM, VEC>(x, a.K);
-      uint32_t t = 0;
+      uint32_t t = 0;  // columns beyond K are still zeros
 #pragma unroll
       for (int i = 0; i < E; ++i) t = max(t, abs_bits(x[i]));
       const RowScale r = row_scale(top(t, tmax));
       if (threadIdx.x == 0) a.x_scale[m] = r.scale;
-      int q[E];
-      i8_codes<E>(x, r, q);
-      store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, q);
+      store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
     }
   }
 }
@@ -119,33 +107,27 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<2 * TEAM>)
   const int64_t m1 = m0 + chunk < g1 ? m0 + chunk : g1;
   if (m0 >= m1) return;
   const T *x0 = static_cast<const T *>(a.X), *dy0 = static_cast<const T *>(a.dY);
-  RawRow<T, TEAM, VEC, E> xn, dn;
-  xn.load(x0 + m0 * a.x_stride, a.K);
-  dn.load(dy0 + m0 * a.dy_stride, a.K);
-  float mean_n = a.mean[m0], rstd_n = a.rstd[m0];
-  float w[E], dw[E], db[E];
-  if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
+  RowsAhead<T, TEAM, VEC, E> xs, ds;
+  xs.start(x0, a.x_stride, m0, m1, a.K);
+  ds.start(dy0, a.dy_stride, m0, m1, a.K);
+  float dw[E], db[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
   const float inv_k = 1.0f / a.K;
   for (int64_t m = m0; m < m1; ++m) {
     float x[E], g[E];
-    xn.values(x);
-    dn.values(g);
-    const float mean = mean_n, rstd = rstd_n;
-    if (m + 1 < m1) {
-      xn.load(x0 + (m + 1) * a.x_stride, a.K);
-      dn.load(dy0 + (m + 1) * a.dy_stride, a.K);
-      mean_n = a.mean[m + 1];
-      rstd_n = a.rstd[m + 1];
-    }
+    const float mean = a.mean[m], rstd = a.rstd[m];
+    xs.take(x0, a.x_stride, m, m1, a.K, x);
+    ds.take(dy0, a.dy_stride, m, m1, a.K, g);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       x[i] = (x[i] - mean) * rstd;  // a column beyond K has g = 0
       dw[i] = fmaf(g[i], x[i], dw[i]);
       db[i] += g[i];
-      if (a.weight) g[i] *= w[i];
     }
+    if (a.weight)
+      with_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K,
+                                [&](int i, float w) { g[i] *= a.weight_offset + w; });
     if (a.dX) {
       float v[2] = {thread_sum(g), thread_dot(g, x)};
       sum(v, turn);
@@ -169,36 +151,32 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<2 * TEAM>)
   }
 }
 
-// dweight and dbias of (group, 32 columns) from the group's slices: eight warps add every eighth slice,
-// then their sums in order.
-__global__ void __launch_bounds__(256) k_layer_norm_slices(NormLaunch a, int slices, int chunk) {
-  __shared__ float part[2][8][32];
-  grid_dep_wait();
+// dweight (blockIdx.z = 0) or dbias (1) of a group's 32 columns from the group's slices: 32 warps add every
+// 32nd slice, then a warp adds their sums in order.
+__global__ void __launch_bounds__(1024) k_layer_norm_slices(NormLaunch a, int slices, int chunk) {
+  __shared__ float part[32][32];
+  float *out = blockIdx.z == 0 ? a.dweight : a.dbias;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = blockIdx.x * 32 + lane;
   const int group = blockIdx.y;
-  const int64_t g0 = static_cast<int64_t>(group) * a.rows_per_group;
-  const int64_t left = a.M - g0;
+  const int64_t left = a.M - static_cast<int64_t>(group) * a.rows_per_group;
   const int rows = left <= 0 ? 0 : static_cast<int>(left < a.rows_per_group ? left : a.rows_per_group);
   const int n = (rows + chunk - 1) / chunk;  // slices that have rows
-  float w = 0.0f, b = 0.0f;
+  grid_dep_wait();
+  if (!out) return;
+  float v = 0.0f;
   if (k < a.K) {
-    const float *p = a.partial + static_cast<size_t>(group) * slices * 2 * a.K + k;
+    const float *p = a.partial + (static_cast<size_t>(group) * slices * 2 + blockIdx.z) * a.K + k;
 #pragma unroll 4
-    for (int s = warp; s < n; s += 8) {
-      w += p[static_cast<size_t>(s) * 2 * a.K];
-      b += p[static_cast<size_t>(s) * 2 * a.K + a.K];
-    }
+    for (int s = warp; s < n; s += 32) v += p[static_cast<size_t>(s) * 2 * a.K];
   }
-  part[0][warp][lane] = w;
-  part[1][warp][lane] = b;
+  part[warp][lane] = v;
   __syncthreads();
-  if (warp < 2 && k < a.K) {
+  if (warp == 0 && k < a.K) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += part[warp][i][lane];
-    float *out = warp == 0 ? a.dweight : a.dbias;
-    if (out) out[static_cast<size_t>(group) * a.K + k] = s;
+    for (int i = 0; i < 32; ++i) s += part[i][lane];
+    out[static_cast<size_t>(group) * a.K + k] = s;
   }
 }
 
@@ -270,7 +248,7 @@ cudaError_t backward_t(const NormLaunch &a) {
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !sums || s.slices == 1) return e;
-  return launch_dependent(k_layer_norm_slices, dim3((a.K + 31) / 32, a.groups), 256, 0, a.stream, a, s.slices, s.chunk);
+  return launch_dependent(k_layer_norm_slices, dim3((a.K + 31) / 32, a.groups, 2), 1024, 0, a.stream, a, s.slices, s.chunk);
 }
 
 }  // namespace

@@ -57,9 +57,10 @@ __global__ void __launch_bounds__(kThreads) k_rope_table(RopeLaunch a, int token
   if (lane >= lanes) return;
   const size_t m0 = static_cast<size_t>(blockIdx.x) * tokens;
   const size_t m1 = m0 + tokens < static_cast<size_t>(a.M) ? m0 + tokens : a.M;
-#pragma unroll 2
+  // four tokens' positions in flight
+#pragma unroll 4
   for (size_t m = m0 + lane; m < m1; m += lanes)
-    reinterpret_cast<float2 *>(a.table)[m * a.n_pairs + p] = ladder(a.pos, m, p);
+    __stcs(reinterpret_cast<float2 *>(a.table) + m * a.n_pairs + p, ladder(a.pos, m, p));
 }
 
 template <typename T>

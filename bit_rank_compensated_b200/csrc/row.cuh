@@ -9,6 +9,7 @@
 
 #include <stdint.h>
 
+#include "i8_quant.cuh"
 #include "svdq.h"
 #include "types.cuh"
 
@@ -95,71 +96,87 @@ __device__ __forceinline__ void store_row(T *p, int K, const float (&y)[E]) {
   }
 }
 
-// The int8 codes of a row: VEC bytes per vector.
+// The int8 codes of a row, VEC bytes a store, each vector as soon as it is formed.
 template <int TEAM, int VEC, int E>
-__device__ __forceinline__ void store_codes(int8_t *p, int K, const int (&q)[E]) {
+__device__ __forceinline__ void store_codes(int8_t *p, int K, const float (&x)[E], const RowScale &r) {
 #pragma unroll
   for (int v = 0; v < E / VEC; ++v) {
     const int k = row_column<TEAM, VEC>(v * VEC);
     if (k >= K) continue;
-    if constexpr (VEC == 1) {
-      p[k] = static_cast<int8_t>(q[v]);
-    } else {
-      uint32_t o[VEC / 4];
+    uint32_t o[(VEC + 3) / 4];
+    i8_pack<VEC>(x + v * VEC, r, o);
+    if constexpr (VEC == 1) p[k] = static_cast<int8_t>(o[0]);
+    else if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p + k) = make_uint2(o[0], o[1]);
+    else *reinterpret_cast<uint32_t *>(p + k) = o[0];
+  }
+}
+
+// VEC parameters (of their own type, aligned to the vector's size where VEC > 1) from element `at` on.
+// They are read again for every row: the rows of a block, and of the SM's other blocks, find them in L1,
+// and the registers stay with the rows in flight.
+template <int VEC>
+__device__ __forceinline__ void load_params(const void *base, int dtype, size_t at, float (&w)[VEC]) {
+  if constexpr (VEC == 1) {
+    w[0] = dtype == SVDQ_F32   ? __ldg(static_cast<const float *>(base) + at)
+           : dtype == SVDQ_F16 ? to_f32(__ldg(static_cast<const __half *>(base) + at))
+                               : to_f32(__ldg(static_cast<const __nv_bfloat16 *>(base) + at));
+  } else if (dtype == SVDQ_F32) {
+    const float *p = static_cast<const float *>(base) + at;
 #pragma unroll
-      for (int e = 0; e < VEC / 4; ++e)
-        o[e] = __byte_perm(__byte_perm(q[VEC * v + 4 * e], q[VEC * v + 4 * e + 1], 0x0040),
-                           __byte_perm(q[VEC * v + 4 * e + 2], q[VEC * v + 4 * e + 3], 0x0040), 0x5410);
-      if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p + k) = make_uint2(o[0], o[1]);
-      else *reinterpret_cast<uint32_t *>(p + k) = o[0];
+    for (int e = 0; e < VEC; e += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4 *>(p + e));
+      w[e] = f.x, w[e + 1] = f.y, w[e + 2] = f.z, w[e + 3] = f.w;
+    }
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+    uint32_t q[VEC / 2];
+    if constexpr (VEC == 8) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+      q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
+    } else {
+      const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+      q[0] = u.x, q[1] = u.y;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      if (dtype == SVDQ_F16) unpack2(q[e], w[2 * e], w[2 * e + 1], __half{});
+      else unpack2(q[e], w[2 * e], w[2 * e + 1], __nv_bfloat16{});
     }
   }
 }
 
-// A parameter row (of its own type, aligned to a vector's size where VEC > 1) in the same columns.
-template <int TEAM, int VEC, int E>
-__device__ __forceinline__ void load_params(const void *base, int dtype, size_t at, int K, float add, float (&w)[E]) {
+// f(i, parameter) for every value i of the thread that exists.
+template <int TEAM, int VEC, int E, typename F>
+__device__ __forceinline__ void with_params(const void *base, int dtype, size_t at, int K, F f) {
 #pragma unroll
   for (int v = 0; v < E / VEC; ++v) {
     const int k = row_column<TEAM, VEC>(v * VEC);
-    if (k >= K) {
+    if (k >= K) continue;
+    float w[VEC];
+    load_params<VEC>(base, dtype, at + k, w);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) w[VEC * v + e] = 0.0f;
-    } else if constexpr (VEC == 1) {
-      w[v] = add + (dtype == SVDQ_F32   ? static_cast<const float *>(base)[at + k]
-                    : dtype == SVDQ_F16 ? to_f32(static_cast<const __half *>(base)[at + k])
-                                        : to_f32(static_cast<const __nv_bfloat16 *>(base)[at + k]));
-    } else if (dtype == SVDQ_F32) {
-      const float *p = static_cast<const float *>(base) + at + k;
-#pragma unroll
-      for (int e = 0; e < VEC; e += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(p + e);
-        w[VEC * v + e] = add + f.x;
-        w[VEC * v + e + 1] = add + f.y;
-        w[VEC * v + e + 2] = add + f.z;
-        w[VEC * v + e + 3] = add + f.w;
-      }
-    } else {
-      const uint16_t *p = static_cast<const uint16_t *>(base) + at + k;
-      uint32_t q[VEC / 2];
-      if constexpr (VEC == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        q[0] = u.x, q[1] = u.y;
-      }
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        float a, b;
-        if (dtype == SVDQ_F16) unpack2(q[e], a, b, __half{});
-        else unpack2(q[e], a, b, __nv_bfloat16{});
-        w[VEC * v + 2 * e] = add + a;
-        w[VEC * v + 2 * e + 1] = add + b;
-      }
-    }
+    for (int e = 0; e < VEC; ++e) f(v * VEC + e, w[e]);
   }
 }
+
+// Rows fetched ahead of the present one: two of 16-bit types, one of fp32 (the same registers).
+template <typename T, int TEAM, int VEC, int E>
+struct RowsAhead {
+  static constexpr int DEPTH = sizeof(T) == 2 && VEC > 1 ? 2 : 1;
+  RawRow<T, TEAM, VEC, E> row[DEPTH];
+
+  __device__ __forceinline__ void start(const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (m0 + d < m1) row[d].load(x0 + (m0 + d) * stride, K);
+  }
+  // row m's values; fetches row m + DEPTH
+  __device__ __forceinline__ void take(const T *x0, size_t stride, int64_t m, int64_t m1, int K, float (&x)[E]) {
+    row[0].values(x);
+    if constexpr (DEPTH == 2) row[0] = row[1];
+    if (m + DEPTH < m1) row[DEPTH - 1].load(x0 + (m + DEPTH) * stride, K);
+  }
+};
 
 // Sums of N values over the block, in every thread and in a fixed order. Consecutive reductions use the
 // two buffers in turn (turn is the caller's count), so one barrier each is enough.

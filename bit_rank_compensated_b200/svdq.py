@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -518,9 +519,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run(name: str, device: torch.device, *args):
-    """Calls an entry point on the tensors' device and its current stream."""
-    index = device.index
+def _run(name: str, t: torch.Tensor, *args):
+    """Calls an entry point on t's device and that device's current stream."""
+    index = t.get_device()
     fn = getattr(_lib or load(), name)
     if index == torch.cuda.current_device():
         status = fn(*args, _raw_stream(index))
@@ -562,7 +563,7 @@ def _vector(t, name: str, n: int, device, dtype=torch.float32):
 def _like(out, X, M: int, K: int, name: str):
     """A caller's output of X's type, checked, or a new one; and its row stride."""
     if out is None:
-        return X.new_empty((M, K)), K
+        return (torch.empty_like(X) if X.is_contiguous() else X.new_empty((M, K))), K
     m, k, stride = _rows(out, name, (X.dtype,))
     if (m, k) != (M, K) or out.device != X.device:
         raise ValueError(f"{name} must be {M} x {K} on {X.device}")
@@ -620,7 +621,7 @@ def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset
     mean = rstd = None
     if stats:
         mean, rstd = X.new_empty((2, M), dtype=torch.float32).unbind(0)
-    _run("svdq_layer_norm", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K, ctypes.addressof(affine), eps,
+    _run("svdq_layer_norm", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K, ctypes.addressof(affine), eps,
          Y.data_ptr(), y_stride, mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None)
     return (Y, mean, rstd) if stats else Y
 
@@ -653,7 +654,7 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0,
         db = sums[-1] if need_dbias else None
     size = load().svdq_layer_norm_workspace_bytes(M, K, n, affine.rows_per_group) if sums is not None else 0
     space, size, kept = _workspace(workspace, size, device)
-    _run("svdq_layer_norm_backward", device, dY.data_ptr(), dy_stride, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+    _run("svdq_layer_norm_backward", X, dY.data_ptr(), dy_stride, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
          ctypes.addressof(affine), _vector(mean, "mean", M, device), _vector(rstd, "rstd", M, device), dx, dx_stride,
          None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), space, size)
     return dX, dw, db
@@ -661,12 +662,17 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0,
 
 def _i8_rows(X, M: int, K: int, xq, x_scale):
     """Int8 rows and scales: the caller's, checked, or new ones; and their addresses."""
-    device = X.device
     if xq is None:
         xq = X.new_empty((M, K), dtype=torch.int8)
+        q = xq.data_ptr()
+    else:
+        q = _vector(xq, "xq", M * K, X.device, torch.int8)
     if x_scale is None:
         x_scale = X.new_empty(M, dtype=torch.float32)
-    return xq, x_scale, _vector(xq, "xq", M * K, device, torch.int8), _vector(x_scale, "x_scale", M, device)
+        s = x_scale.data_ptr()
+    else:
+        s = _vector(x_scale, "x_scale", M, X.device)
+    return xq, x_scale, q, s
 
 
 def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
@@ -676,7 +682,7 @@ def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
         return _on_stream(stream, i8_quantize_rows, X, col_scale, xq, x_scale)
     M, K, x_stride = _rows(X, "X")
     xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
-    _run("svdq_i8_quantize_rows", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+    _run("svdq_i8_quantize_rows", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
          _vector(col_scale, "col_scale", K, X.device), q, s)
     return xq, x_scale
 
@@ -690,7 +696,7 @@ def i8_layer_norm_quantize(X, weight=None, bias=None, rows_per_group: int = 0, w
     M, K, x_stride = _rows(X, "X")
     affine = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
     xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
-    _run("svdq_i8_layer_norm_quantize", X.device, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
+    _run("svdq_i8_layer_norm_quantize", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
          ctypes.addressof(affine), eps, q, s)
     return xq, x_scale
 
@@ -704,7 +710,7 @@ def _i8_weight(wq, w_scale, bias, K: int, device):
         raise ValueError(f"wq must be a matrix of {K} columns")
     N = wq.shape[0]
     return (N, _vector(wq, "wq", N * K, device, torch.int8), _vector(w_scale, "w_scale", N, device),
-            _vector(bias, "bias", N, device))
+            None if bias is None else _vector(bias, "bias", N, device))
 
 
 def i8_gemm(xq, x_scale, wq, w_scale, bias=None, Y=None, dtype=torch.bfloat16, workspace=None, stream=None):
@@ -719,29 +725,49 @@ def i8_gemm(xq, x_scale, wq, w_scale, bias=None, Y=None, dtype=torch.bfloat16, w
     x, xs = _vector(xq, "xq", M * K, device, torch.int8), _vector(x_scale, "x_scale", M, device)
     if Y is None:
         Y = xq.new_empty((M, N), dtype=dtype)
-    y = _vector(Y, "Y", M * N, device, dtype)
+        y = Y.data_ptr()
+    else:
+        y = _vector(Y, "Y", M * N, device, dtype)
     space, size, kept = _workspace(workspace, load().svdq_i8_workspace_bytes(M, N, K), device)
-    _run("svdq_i8_gemm", device, x, xs, M, w, ws, b, N, K, y, DTYPES[dtype], space, size)
+    _run("svdq_i8_gemm", xq, x, xs, M, w, ws, b, N, K, y, DTYPES[dtype], space, size)
     return Y
 
 
 def i8_linear_forward(X, wq, w_scale, bias=None, col_scale=None, xq=None, x_scale=None, Y=None, workspace=None,
                       stream=None):
     """The 8-bit linear of X [M, K]: rows quantized (under the smoothing col_scale, if any), then i8_gemm;
-    Y has X's type."""
+    Y has X's type. xq, x_scale and workspace are scratch of the sizes that i8_quantize_rows returns and
+    i8_workspace_bytes says."""
     if stream is not None:
         return _on_stream(stream, i8_linear_forward, X, wq, w_scale, bias, col_scale, xq, x_scale, Y, workspace)
     M, K, x_stride = _rows(X, "X")
     device = X.device
     N, w, ws, b = _i8_weight(wq, w_scale, bias, K, device)
-    xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
+    size = load().svdq_i8_workspace_bytes(M, N, K)
+    if xq is None and x_scale is None and workspace is None:
+        # one allocation: the rows (a multiple of 16 bytes), the workspace, the scales
+        rows = M * K
+        kept = X.new_empty(rows + size + 4 * M, dtype=torch.int8)
+        q = kept.data_ptr()
+        space = q + rows if size else None
+        s = q + rows + size
+    else:
+        xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
+        space, size, kept = _workspace(workspace, size, device)
     if Y is None:
         Y = X.new_empty((M, N))
-    y = _vector(Y, "Y", M * N, device, X.dtype)
-    space, size, kept = _workspace(workspace, load().svdq_i8_workspace_bytes(M, N, K), device)
-    _run("svdq_i8_linear_forward", device, X.data_ptr(), x_stride, DTYPES[X.dtype], M,
-         _vector(col_scale, "col_scale", K, device), w, ws, b, N, K, q, s, y, space, size)
+        y = Y.data_ptr()
+    else:
+        y = _vector(Y, "Y", M * N, device, X.dtype)
+    _run("svdq_i8_linear_forward", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M,
+         None if col_scale is None else _vector(col_scale, "col_scale", K, device), w, ws, b, N, K, q, s, y, space, size)
     return Y
+
+
+# svdq_rope_axes, svdq_positions and svdq_heads as bytes in the C layout (quicker to make than ctypes structs)
+_ROPE_AXES = struct.Struct("@7if")
+_POSITIONS = struct.Struct("@PiNN")
+_HEADS = struct.Struct("@PiNN")
 
 
 class RopeAxes:
@@ -756,8 +782,7 @@ class RopeAxes:
             raise ValueError("one to four axes of at least one pair are supported")
         self.pairs, self.theta = tuple(pairs), float(theta)
         self.n_pairs = sum(pairs)
-        self.s = RopeAxesStruct(len(pairs), self.pairs, bool(shared_ladder), bool(halves), self.theta)
-        self.address = ctypes.addressof(self.s)
+        self.s = _ROPE_AXES.pack(len(pairs), *self.pairs, *(0,) * (4 - len(pairs)), bool(shared_ladder), bool(halves), theta)
 
 
 def _positions(pos, axes: RopeAxes, M=None, device=None):
@@ -769,7 +794,7 @@ def _positions(pos, axes: RopeAxes, M=None, device=None):
             or (device is not None and pos.device != device)):
         raise ValueError(f"pos must be [tokens, {len(axes.pairs)}], with the heads' tokens and device")
     token, axis = pos.stride()
-    return PositionsStruct(pos.data_ptr(), DTYPES[pos.dtype], token, axis)
+    return _POSITIONS.pack(pos.data_ptr(), DTYPES[pos.dtype], token, axis)
 
 
 def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
@@ -781,30 +806,28 @@ def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
     M, n = pos.shape[0], axes.n_pairs
     if table is None:
         table = pos.new_empty((M, n, 2), dtype=torch.float32)
-    _run("svdq_rope_axes_table", pos.device, ctypes.addressof(p), M, axes.address,
-         _vector(table, "table", 2 * M * n, pos.device))
+        to = table.data_ptr()
+    else:
+        to = _vector(table, "table", 2 * M * n, pos.device)
+    _run("svdq_rope_axes_table", pos, p, M, axes.s, to)
     return table
 
 
-def _heads(t, out, name: str, like):
-    """The C structs of heads [M, H, D] and of their output (a new one unless given)."""
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype not in _FLOATS
-            or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must be [tokens, heads, columns] on a GPU, of one floating type and device with q")
-    M, H, D = t.shape
-    if M != like.shape[0] or D != like.shape[2]:
-        raise ValueError(f"{name} must have q's tokens and columns")
+def _heads(t, out, name: str, M: int, D: int, dtype, device):
+    """svdq_heads of heads [M, H, D] and of their output, and the output (a new one unless given)."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[0] != M or t.shape[2] != D:
+        raise ValueError(f"{name} must be [{M}, heads, {D}] of {dtype} on {device}")
     token, head, one = t.stride()
+    H = t.shape[1]
+    source = _HEADS.pack(t.data_ptr(), H, token, head)
     if out is None:
-        out = t.new_empty((M, H, D))
-        to = (H * D, D, 1)
-    else:
-        if out.shape != t.shape or out.dtype != t.dtype or out.device != t.device:
-            raise ValueError(f"{name}_out must be like {name}")
-        to = out.stride()
-    if one != 1 or to[2] != 1:
+        out = torch.empty_like(t)
+    elif out.shape != t.shape or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{name}_out must be like {name}")
+    token, head, last = out.stride()
+    if one != 1 or last != 1:
         raise ValueError(f"the columns of {name} and its output must be contiguous")
-    return HeadsStruct(t.data_ptr(), H, token, head), HeadsStruct(out.data_ptr(), H, to[0], to[1]), out
+    return source, _HEADS.pack(out.data_ptr(), H, token, head), out
 
 
 def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -813,17 +836,17 @@ def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None
     be q and k. Returns (q_out, k_out)."""
     if stream is not None:
         return _on_stream(stream, rope_axes_apply, q, k, pos, axes, inverse, q_out, k_out)
-    at = ctypes.addressof
-    qi, qo, q_out = _heads(q, q_out, "q", q)
-    ki = ko = None
-    if k is not None:
-        ki, ko, k_out = _heads(k, k_out, "k", q)
-    else:
-        k_out = None
+    dtype, device = q.dtype, q.device
+    if q.dim() != 3 or not q.is_cuda or dtype not in _FLOATS:
+        raise ValueError("q must be a CUDA tensor [tokens, heads, columns] of a floating type of 16 or 32 bits")
     M, _, D = q.shape
-    p = _positions(pos, axes, M, q.device)
-    _run("svdq_rope_axes_apply", q.device, at(qi), at(qo), ki and at(ki), ko and at(ko), DTYPES[q.dtype], M, D, at(p),
-         axes.address, bool(inverse))
+    qi, qo, q_out = _heads(q, q_out, "q", M, D, dtype, device)
+    if k is None:
+        ki = ko = k_out = None
+    else:
+        ki, ko, k_out = _heads(k, k_out, "k", M, D, dtype, device)
+    p = _positions(pos, axes, M, device)
+    _run("svdq_rope_axes_apply", q, qi, qo, ki, ko, DTYPES[dtype], M, D, p, axes.s, bool(inverse))
     return q_out, k_out
 
 
