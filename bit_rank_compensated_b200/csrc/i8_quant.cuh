@@ -1,72 +1,76 @@
-// The int8 row quantizer's arithmetic, shared by the row quantizer and the layer norm's int8 form.
+// The int8 row quantizer's arithmetic, shared by the row quantizer, the layer norm's int8 form and the
+// 8-bit linear of few tokens.
 #pragma once
 
 #include <stdint.h>
 
-namespace svdq {
+#include "pair.cuh"
 
-// |v| as an integer: ordered like |v| for finite values, infinities and NaNs above all of them.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+namespace svdq {
 
 struct RowScale {
   float scale;  // max / 127; NaN for a row with an infinity or a NaN
-  float by;     // power of two that brings the row's values where the arithmetic below is exact
-  float top;    // by * max |v| of a finite row, else 0
+  float c;      // about 127 / max; NaN where that is no fit for fp32 (every code then takes the exact way)
+  float by;     // power of two that brings the row's values where the exact way's arithmetic is exact
+  float top;    // by * max
   float inv;    // about 127 / top; 0 for a row of zeros or of no finite maximum
 };
 
+// top_bits: the bits of the row's largest |v| (infinities and NaNs above all others).
 __device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
-  if (top_bits >= 0x7f800000u) return {__uint_as_float(0x7fffffffu), 0.0f, 0.0f, 0.0f};
+  const float nan = __uint_as_float(0x7fffffffu);
+  if (top_bits >= 0x7f800000u) return {nan, nan, 0.0f, 0.0f, 0.0f};
   const float max = __uint_as_float(top_bits);
   const float by = max < 0x1p-60f ? 0x1p90f : (max > 0x1p100f ? 0x1p-30f : 1.0f);
   const float top = max * by;
-  return {__fdiv_rn(max, 127.0f), by, top, top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f};
+  const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
+  return {__fdiv_rn(max, 127.0f), by == 1.0f ? inv : nan, by, top, inv};
 }
 
-// Whether the fp32 product t = v * (127 / top) decides the code: it is within 127 * 2^-22 < 2^-14 of the
-// quotient, so it does unless it lies that near to a border.
-__device__ __forceinline__ bool i8_decided(float t, float n) { return fabsf(t - n) < 0.4999f; }
-
-// The code of a value near a border k + 1/2, from the exact comparison of 127 |v| with (k + 1/2) top: the
-// former is p + e (a product and its rounding error), and (k + 1/2) top - p, of 32 bits of which 12 at
-// least cancel, is exact in one fma. A tie goes to the even code.
-__device__ __forceinline__ int i8_code_exact(float v, float t, float top) {
-  const float a = fabsf(v), k = floorf(fabsf(t));
-  const float p = __fmul_rn(a, 127.0f), e = __fmaf_rn(a, 127.0f, -p);
-  const float d = __fmaf_rn(k + 0.5f, top, -p);
-  const int n = static_cast<int>(k);
-  const int c = d > e ? n : (d < e ? n + 1 : n + (n & 1));
-  return v < 0.0f ? -c : c;
-}
-
-// rint(127 v / max), ties to even, as the exact quotient rounds.
+// rint(127 v / max), ties to even, as the exact quotient rounds: with k below the quotient, 127 |v| is
+// compared with (k + 1/2) top. The former is p + e (a product and its rounding error); near the border
+// (k + 1/2) top - p, of 32 bits of which 12 at least cancel, is exact in one fma.
 __device__ __forceinline__ int i8_code(float v, const RowScale &r) {
   if (r.inv == 0.0f) return 0;
   const float x = v * r.by, t = x * r.inv, n = rintf(t);
-  return i8_decided(t, n) ? static_cast<int>(n) : i8_code_exact(x, t, r.top);
+  if (fabsf(t - n) < 0.4999f) return static_cast<int>(n);
+  const float a = fabsf(x), k = floorf(fabsf(t));
+  const float p = __fmul_rn(a, 127.0f), e = __fmaf_rn(a, 127.0f, -p);
+  const float d = __fmaf_rn(k + 0.5f, r.top, -p);
+  const int i = static_cast<int>(k);
+  const int c = d > e ? i : (d < e ? i + 1 : i + (i & 1));  // a tie goes to the even code
+  return x < 0.0f ? -c : c;
 }
 
-// Codes of VEC values, the first in the lowest byte of o[0]. Hardly any value lies near a border: one test
-// for all of them.
-template <int VEC>
-__device__ __forceinline__ void i8_pack(const float *v, const RowScale &r, uint32_t (&o)[(VEC + 3) / 4]) {
-  int q[VEC];
-  bool decided = true;
+// Codes of 2 N values, the first in the lowest byte of o[0] (N = 1: both in o[0]). Adding 1.5 * 2^23 rounds
+// v c to an integer whose last byte is the code; v c is within 127 * 2^-23 of the quotient, so that
+// decides unless v c lies that near to a border (0.4999 of a step from the integer): hardly any value
+// does, and one test serves them all.
+template <int N>
+__device__ __forceinline__ void i8_pack(const f32x2 *v, const RowScale &r, uint32_t (&o)[(N + 1) / 2]) {
+  const f32x2 c = both(r.c), magic = both(12582912.0f);
+  uint32_t q[2 * N];
+  float far = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const float t = v[i] * r.by * r.inv, n = rintf(t);
-    decided = decided && i8_decided(t, n);
-    q[i] = static_cast<int>(n);
+  for (int i = 0; i < N; ++i) {
+    const f32x2 s = fma2(v[i], c, magic);
+    const f32x2 d = fma2(v[i], c, sub2(magic, s));  // v c - n
+    q[2 * i] = lo_bits(s);
+    q[2 * i + 1] = hi_bits(s);
+    far = max_abs3(far, lo(d), hi(d));
   }
-  if (!decided) {  // (NaNs of a row without a finite maximum too)
+  if (!(far < 0.4999f)) {  // a value near a border, or a row without a c
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) q[i] = i8_code(v[i], r);
+    for (int i = 0; i < N; ++i) {
+      q[2 * i] = static_cast<uint32_t>(i8_code(lo(v[i]), r));
+      q[2 * i + 1] = static_cast<uint32_t>(i8_code(hi(v[i]), r));
+    }
   }
-  if constexpr (VEC == 1) {
-    o[0] = static_cast<uint32_t>(q[0]);
+  if constexpr (N == 1) {
+    o[0] = __byte_perm(q[0], q[1], 0x0040);
   } else {
 #pragma unroll
-    for (int e = 0; e < VEC / 4; ++e)
+    for (int e = 0; e < N / 2; ++e)
       o[e] = __byte_perm(__byte_perm(q[4 * e], q[4 * e + 1], 0x0040), __byte_perm(q[4 * e + 2], q[4 * e + 3], 0x0040), 0x5410);
   }
 }

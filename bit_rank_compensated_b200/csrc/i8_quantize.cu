@@ -8,8 +8,12 @@
 namespace svdq {
 namespace {
 
+// Registers for the row, its smoothing and two rows ahead.
+template <int TEAM>
+constexpr int kBlocks = blocks_per_sm(TEAM, 1024);
+
 template <typename T, int TEAM, int E, int VEC>
-__global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_quantize_rows(QuantRowsLaunch a, int rows_per_block) {
+__global__ void __launch_bounds__(TEAM, kBlocks<TEAM>) k_quantize_rows(QuantRowsLaunch a, int rows_per_block) {
   __shared__ BlockMax<TEAM> top;
   grid_dep_wait();
   grid_dep_launch();
@@ -17,17 +21,18 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_quantize_rows(Quan
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  RowsAhead<T, TEAM, VEC, E> ahead;
+  RowsAhead<T, TEAM, VEC, E, (sizeof(T) == 2 && VEC > 1) ? 2 : 1> ahead;
   ahead.start(x0, a.x_stride, m0, m1, a.K);
-  for (int64_t m = m0; m < m1; ++m) {
-    float x[E];
-    ahead.take(x0, a.x_stride, m, m1, a.K, x);
-    if (a.col_scale)
-      with_params<TEAM, VEC, E>(a.col_scale, SVDQ_F32, 0, a.K, [&](int i, float c) { x[i] = __fmul_rn(x[i], c); });
-    uint32_t t = 0;  // columns beyond K are zeros
+  f32x2 c[E / 2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) t = max(t, abs_bits(x[i]));
-    const RowScale r = row_scale(top(t, turn));
+  for (int i = 0; i < E / 2; ++i) c[i] = both(1.0f);  // exact
+  if (a.col_scale) load_params<TEAM, VEC, E>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
+  for (int64_t m = m0; m < m1; ++m) {
+    f32x2 x[E / 2];
+    ahead.take(x0, a.x_stride, m, m1, a.K, x);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c[i]);
+    const RowScale r = row_scale(top(thread_top(x), turn));
     if (threadIdx.x == 0) a.x_scale[m] = r.scale;
     store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
   }
@@ -41,7 +46,7 @@ __global__ void __launch_bounds__(1024) k_quantize_long_rows(QuantRowsLaunch a) 
   const T *x = static_cast<const T *>(a.X) + m * a.x_stride;
   auto value = [&](int k) { return a.col_scale ? __fmul_rn(to_f32(x[k]), a.col_scale[k]) : to_f32(x[k]); };
   uint32_t t = 0, turn = 0;
-  for (int k = threadIdx.x; k < a.K; k += 1024) t = max(t, abs_bits(value(k)));
+  for (int k = threadIdx.x; k < a.K; k += 1024) t = max(t, __float_as_uint(value(k)) & 0x7fffffffu);
   const RowScale r = row_scale(top(t, turn));
   if (threadIdx.x == 0) a.x_scale[m] = r.scale;
   for (int k = threadIdx.x; k < a.K; k += 1024) a.xq[m * a.K + k] = static_cast<int8_t>(i8_code(value(k), r));
@@ -56,7 +61,7 @@ cudaError_t quantize_t(const QuantRowsLaunch &a) {
   const bool vec = a.K % kVec<T> == 0 && rows_aligned(a.X, a.M > 1 ? a.x_stride : 0, sizeof(T), 16) &&
                    rows_aligned(a.col_scale, 0, 4, 16);
   return for_row(a.K, [&]<int TEAM, int E>() {
-    const int blocks = a.num_sms * kBlocksPerSm<TEAM>;
+    const int blocks = a.num_sms * kBlocks<TEAM>;
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
     if (vec) return launch_dependent(k_quantize_rows<T, TEAM, E, kVec<T>>, grid, TEAM, 0, a.stream, a, rows);

@@ -6,7 +6,9 @@
 // All three are bound by memory: one read of each input row and one write of each output row. A row
 // lives in the registers of one block (row.cuh), so x is read once although mean, variance (about the
 // mean, not from squares), the maximum for int8 and the output each need it; a block walks consecutive
-// rows with the next rows' loads in flight while it reduces the present one, and finds weights in L1.
+// rows with its columns' weights in registers and the next rows' loads in flight while it reduces the
+// present one. Packed fp32 instructions (pair.cuh) keep the issue slots of a row below the time its
+// bytes take.
 //
 // The gradient's column sums run in the same pass: a block adds its rows' dy xhat and dy into registers
 // (each thread its own columns: no atomics, a fixed order) and writes one slice of partial sums; a
@@ -18,32 +20,16 @@
 namespace svdq {
 namespace {
 
-template <int E, int TEAM, int VEC>
-__device__ __forceinline__ void no_columns_beyond(float (&d)[E], int K) {
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (row_column<TEAM, VEC>(i) >= K) d[i] = 0.0f;
-}
-
-// A tree of additions within the thread: the sum's longest chain stays short.
-template <int E>
-__device__ __forceinline__ float thread_sum(const float (&x)[E]) {
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < E; ++i) s[i & 3] += x[i];
-  return (s[0] + s[1]) + (s[2] + s[3]);
-}
-template <int E>
-__device__ __forceinline__ float thread_dot(const float (&x)[E], const float (&y)[E]) {
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < E; ++i) s[i & 3] = fmaf(x[i], y[i], s[i & 3]);
-  return (s[0] + s[1]) + (s[2] + s[3]);
-}
+// Threads on an SM: registers for the row, its weight and bias and two rows ahead; a row of 1024
+// threads has too few registers for that and reads its weights again for every row (from L1).
+template <int TEAM>
+constexpr int kForwardBlocks = blocks_per_sm(TEAM, 768);
+template <int TEAM>
+constexpr bool kKeepParams = TEAM < 1024;
 
 // Forward: rows [block's first, last) of X; QUANT writes int8 rows and their scales instead of Y.
 template <typename T, int TEAM, int E, int VEC, bool QUANT>
-__global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLaunch a, int rows_per_block) {
+__global__ void __launch_bounds__(TEAM, kForwardBlocks<TEAM>) k_layer_norm(NormLaunch a, int rows_per_block) {
   __shared__ BlockSum<TEAM, 1> sum;
   __shared__ BlockMax<TEAM> top;
   grid_dep_wait();
@@ -52,19 +38,30 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLau
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  RowsAhead<T, TEAM, VEC, E> ahead;
+  RowsAhead<T, TEAM, VEC, E, (sizeof(T) == 2 && VEC > 1 && TEAM < 1024) ? 2 : 1> ahead;
   ahead.start(x0, a.x_stride, m0, m1, a.K);
+  f32x2 w[E / 2], b[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    w[i] = both(1.0f);
+    b[i] = 0;
+  }
+  int64_t group_end = m0;  // first row of the next group
   const float inv_k = 1.0f / a.K;
   for (int64_t m = m0; m < m1; ++m) {
-    float x[E];
+    f32x2 x[E / 2];
     ahead.take(x0, a.x_stride, m, m1, a.K, x);
-    const size_t group = static_cast<int>(m) / a.rows_per_group;
-    float v[1] = {thread_sum(x)};  // columns beyond K are zeros
+    if (m >= group_end || !kKeepParams<TEAM>) {
+      const size_t group = static_cast<uint32_t>(m) / static_cast<uint32_t>(a.rows_per_group);
+      group_end = static_cast<int64_t>(group + 1) * a.rows_per_group;
+      if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
+      if (a.bias) load_params<TEAM, VEC, E>(a.bias, a.param_dtype, group * a.bias_stride, a.K, 0.0f, b);
+    }
+    float v[1] = {thread_sum(x)};
     sum(v, turn);
     const float mean = v[0] * inv_k;
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] -= mean;
-    no_columns_beyond<E, TEAM, VEC>(x, a.K);
+    const f32x2 minus = both(-mean);
+    within_row<TEAM, VEC, E>(a.K, x, [&](f32x2 p, int) { return add2(p, minus); });
     v[0] = thread_dot(x, x);
     sum(v, turn);
     const float rstd = 1.0f / sqrtf(fmaf(v[0], inv_k, a.eps));
@@ -72,20 +69,14 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLau
       if (a.mean) a.mean[m] = mean;
       if (a.rstd) a.rstd[m] = rstd;
     }
+    const f32x2 r2 = both(rstd);
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] *= rstd;
-    if (a.weight)
-      with_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K,
-                                [&](int i, float w) { x[i] *= a.weight_offset + w; });
-    if (a.bias)
-      with_params<TEAM, VEC, E>(a.bias, a.param_dtype, group * a.bias_stride, a.K, [&](int i, float b) { x[i] += b; });
+    for (int i = 0; i < E / 2; ++i) x[i] = fma2(mul2(x[i], r2), w[i], b[i]);
     if constexpr (!QUANT) {
       store_row<T, TEAM, VEC, E>(static_cast<T *>(a.Y) + m * a.y_stride, a.K, x);
     } else {
-      uint32_t t = 0;  // columns beyond K are still zeros
-#pragma unroll
-      for (int i = 0; i < E; ++i) t = max(t, abs_bits(x[i]));
-      const RowScale r = row_scale(top(t, tmax));
+      // columns from K on are zeros still: their x and b are
+      const RowScale r = row_scale(top(thread_top(x), tmax));
       if (threadIdx.x == 0) a.x_scale[m] = r.scale;
       store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
     }
@@ -94,9 +85,11 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<TEAM>) k_layer_norm(NormLau
 
 // Gradient: block (group g, slice s) takes rows [chunk s of the group]. Partial sums go to
 // partial[block][2][K], or straight to dweight and dbias where a group has one slice.
+template <int TEAM>
+constexpr int kBackwardBlocks = blocks_per_sm(TEAM, 512);
+
 template <typename T, int TEAM, int E, int VEC>
-__global__ void __launch_bounds__(TEAM, kBlocksPerSm<2 * TEAM>)
-    k_layer_norm_backward(NormLaunch a, int slices, int chunk) {
+__global__ void __launch_bounds__(TEAM, kBackwardBlocks<TEAM>) k_layer_norm_backward(NormLaunch a, int slices, int chunk) {
   __shared__ BlockSum<TEAM, 2> sum;
   grid_dep_launch();
   uint32_t turn = 0;
@@ -107,33 +100,41 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<2 * TEAM>)
   const int64_t m1 = m0 + chunk < g1 ? m0 + chunk : g1;
   if (m0 >= m1) return;
   const T *x0 = static_cast<const T *>(a.X), *dy0 = static_cast<const T *>(a.dY);
-  RowsAhead<T, TEAM, VEC, E> xs, ds;
+  RowsAhead<T, TEAM, VEC, E, 1> xs, ds;
   xs.start(x0, a.x_stride, m0, m1, a.K);
   ds.start(dy0, a.dy_stride, m0, m1, a.K);
-  float dw[E], db[E];
+  float mean_n = a.mean[m0], rstd_n = a.rstd[m0];
+  f32x2 w[E / 2], dw[E / 2], db[E / 2];
 #pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
+  for (int i = 0; i < E / 2; ++i) {
+    dw[i] = db[i] = 0;
+    w[i] = both(1.0f);
+  }
+  if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
   const float inv_k = 1.0f / a.K;
   for (int64_t m = m0; m < m1; ++m) {
-    float x[E], g[E];
-    const float mean = a.mean[m], rstd = a.rstd[m];
+    f32x2 x[E / 2], g[E / 2];
     xs.take(x0, a.x_stride, m, m1, a.K, x);
     ds.take(dy0, a.dy_stride, m, m1, a.K, g);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      x[i] = (x[i] - mean) * rstd;  // a column beyond K has g = 0
-      dw[i] = fmaf(g[i], x[i], dw[i]);
-      db[i] += g[i];
+    const f32x2 minus = both(-mean_n), r2 = both(rstd_n);
+    const float rstd = rstd_n;
+    if (m + 1 < m1) {
+      mean_n = a.mean[m + 1];
+      rstd_n = a.rstd[m + 1];
     }
-    if (a.weight)
-      with_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K,
-                                [&](int i, float w) { g[i] *= a.weight_offset + w; });
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      x[i] = mul2(add2(x[i], minus), r2);  // a column from K on has g = 0
+      dw[i] = fma2(g[i], x[i], dw[i]);
+      db[i] = add2(db[i], g[i]);
+      g[i] = mul2(g[i], w[i]);
+    }
     if (a.dX) {
       float v[2] = {thread_sum(g), thread_dot(g, x)};
       sum(v, turn);
-      const float c0 = v[0] * inv_k, c1 = v[1] * inv_k;
+      const f32x2 c0 = both(-v[0] * inv_k * rstd), c1 = both(-v[1] * inv_k * rstd);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = rstd * (g[i] - fmaf(x[i], c1, c0));
+      for (int i = 0; i < E / 2; ++i) x[i] = fma2(g[i], r2, fma2(x[i], c1, c0));
       store_row<T, TEAM, VEC, E>(static_cast<T *>(a.dX) + m * a.dx_stride, a.K, x);
     }
   }
@@ -145,8 +146,8 @@ __global__ void __launch_bounds__(TEAM, kBlocksPerSm<2 * TEAM>)
   for (int i = 0; i < E; ++i) {
     const int k = row_column<TEAM, VEC>(i);
     if (k < a.K) {
-      if (pw) pw[at + k] = dw[i];
-      if (pb) pb[at + k] = db[i];
+      if (pw) pw[at + k] = i % 2 ? hi(dw[i / 2]) : lo(dw[i / 2]);
+      if (pb) pb[at + k] = i % 2 ? hi(db[i / 2]) : lo(db[i / 2]);
     }
   }
 }
@@ -197,7 +198,7 @@ template <typename T, bool QUANT>
 cudaError_t forward_t(const NormLaunch &a) {
   return for_row(a.K, [&]<int TEAM, int E>() {
     // a block's rows are consecutive: as many blocks as are resident at once
-    const int blocks = a.num_sms * kBlocksPerSm<TEAM>;
+    const int blocks = a.num_sms * kForwardBlocks<TEAM>;
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
     if (vectors<T>(a)) return launch_dependent(k_layer_norm<T, TEAM, E, kVec<T>, QUANT>, grid, TEAM, 0, a.stream, a, rows);
@@ -212,8 +213,8 @@ cudaError_t forward(const NormLaunch &a) {
   return forward_t<__nv_bfloat16, QUANT>(a);
 }
 
-// Slices of a group's rows in the backward pass and the rows of each: about two resident blocks of 512
-// threads for every SM over all groups, but no slice under four rows, whose partial sums would weigh
+// Slices of a group's rows in the backward pass and the rows of each: the blocks that the SMs hold at once,
+// over all groups, but no slice under four rows, whose partial sums would weigh
 // as much as the rows themselves.
 struct Slices {
   int slices, chunk;
@@ -221,8 +222,7 @@ struct Slices {
 Slices slices_of(int M, int K, int rows_per_group) {
   const int used = (M + rows_per_group - 1) / rows_per_group;
   const int rows = M < rows_per_group ? M : rows_per_group;
-  const int team = for_row(K, []<int TEAM, int>() { return TEAM; });
-  const int blocks = 148 * (512 / team > 8 ? 8 : (512 / team < 1 ? 1 : 512 / team));
+  const int blocks = 148 * for_row(K, []<int TEAM, int>() { return kBackwardBlocks<TEAM>; });
   int s = blocks / used;
   if (s > (rows + 3) / 4) s = (rows + 3) / 4;
   if (s < 1) s = 1;

@@ -90,7 +90,11 @@ struct Vec {
   __device__ __forceinline__ void get(float (&x)[VEC]) const {
     if constexpr (VEC == 8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) unpack2(w[i], x[2 * i], x[2 * i + 1], T{});
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 p = widen(w[i], T{});
+        x[2 * i] = lo(p);
+        x[2 * i + 1] = hi(p);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) x[i] = __uint_as_float(w[i]);
@@ -100,7 +104,7 @@ struct Vec {
   __device__ __forceinline__ void set(const float (&x)[VEC]) {
     if constexpr (VEC == 8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_pair(x[2 * i], x[2 * i + 1], T{});
+      for (int i = 0; i < 4; ++i) w[i] = narrow(pair(x[2 * i], x[2 * i + 1]), T{});
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(x[i]);

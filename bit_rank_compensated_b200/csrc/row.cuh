@@ -1,15 +1,15 @@
 // A row spread over the threads of a block, in registers: what the layer norm's kernels and the row
 // quantizer share.
 //
-// Thread t of TEAM holds E values: VEC consecutive ones at columns (v TEAM + t) VEC, v = 0 ..
+// Thread t of TEAM holds E values as E / 2 pairs: VEC consecutive ones at columns (v TEAM + t) VEC, v = 0 ..
 // E / VEC - 1, VEC values being 16 bytes (one load), or VEC = 1 where rows do not start on 16 bytes or
-// do not end on a whole vector (consecutive threads on consecutive columns). Columns from K on are
-// no one's: value(i) tells whether value i exists.
+// do not end on a whole vector (consecutive threads on consecutive columns). Columns from K on hold zeros.
 #pragma once
 
 #include <stdint.h>
 
 #include "i8_quant.cuh"
+#include "pair.cuh"
 #include "svdq.h"
 #include "types.cuh"
 
@@ -23,21 +23,18 @@ __device__ __forceinline__ int row_column(int i) {
   return ((i / VEC) * TEAM + static_cast<int>(threadIdx.x)) * VEC + i % VEC;
 }
 
-__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b, __nv_bfloat16) {
-  a = __uint_as_float(w << 16);
-  b = __uint_as_float(w & 0xffff0000u);
-}
-__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b, __half) {
+// Two 16-bit values of a word as fp32, and back.
+__device__ __forceinline__ f32x2 widen(uint32_t w, __nv_bfloat16) { return pair_bits(w << 16, w & 0xffff0000u); }
+__device__ __forceinline__ f32x2 widen(uint32_t w, __half) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-  a = f.x;
-  b = f.y;
+  return pair(f.x, f.y);
 }
-__device__ __forceinline__ uint32_t pack_pair(float a, float b, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t narrow(f32x2 v, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo(v), hi(v));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t pack_pair(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t narrow(f32x2 v, __half) {
+  const __half2 h = __floats2half2_rn(lo(v), hi(v));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
@@ -66,103 +63,132 @@ struct RawRow {
       }
     }
   }
-  __device__ __forceinline__ void values(float (&x)[E]) const {
-    if constexpr (VEC > 1 && sizeof(T) == 2) {
+  __device__ __forceinline__ void values(f32x2 (&x)[E / 2]) const {
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) unpack2(w[i], x[2 * i], x[2 * i + 1], T{});
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < E / 2; ++i) {
+      if constexpr (VEC > 1 && sizeof(T) == 2) x[i] = widen(w[i], T{});
+      else x[i] = pair_bits(w[2 * i], w[2 * i + 1]);
     }
   }
 };
 
 template <typename T, int TEAM, int VEC, int E>
-__device__ __forceinline__ void store_row(T *p, int K, const float (&y)[E]) {
+__device__ __forceinline__ void store_row(T *p, int K, const f32x2 (&y)[E / 2]) {
+  if constexpr (VEC == 1) {
 #pragma unroll
-  for (int v = 0; v < E / VEC; ++v) {
-    const int k = row_column<TEAM, VEC>(v * VEC);
-    if (k >= K) continue;
-    if constexpr (VEC == 1) {
-      p[k] = from_f32<T>(y[v]);
-    } else if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4 *>(p + k) = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
-    } else {
-      uint32_t o[4];
+    for (int i = 0; i < E; ++i) {
+      const int k = row_column<TEAM, VEC>(i);
+      if (k < K) p[k] = from_f32<T>(i % 2 ? hi(y[i / 2]) : lo(y[i / 2]));
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = pack_pair(y[8 * v + 2 * e], y[8 * v + 2 * e + 1], T{});
-      *reinterpret_cast<uint4 *>(p + k) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int v = 0; v < E / VEC; ++v) {
+      const int k = row_column<TEAM, VEC>(v * VEC);
+      if (k >= K) continue;
+      const f32x2 *s = y + v * VEC / 2;
+      uint4 o;
+      if constexpr (sizeof(T) == 4) o = make_uint4(lo_bits(s[0]), hi_bits(s[0]), lo_bits(s[1]), hi_bits(s[1]));
+      else o = make_uint4(narrow(s[0], T{}), narrow(s[1], T{}), narrow(s[2], T{}), narrow(s[3], T{}));
+      *reinterpret_cast<uint4 *>(p + k) = o;
     }
   }
 }
 
 // The int8 codes of a row, VEC bytes a store, each vector as soon as it is formed.
 template <int TEAM, int VEC, int E>
-__device__ __forceinline__ void store_codes(int8_t *p, int K, const float (&x)[E], const RowScale &r) {
+__device__ __forceinline__ void store_codes(int8_t *p, int K, const f32x2 (&x)[E / 2], const RowScale &r) {
 #pragma unroll
-  for (int v = 0; v < E / VEC; ++v) {
-    const int k = row_column<TEAM, VEC>(v * VEC);
-    if (k >= K) continue;
-    uint32_t o[(VEC + 3) / 4];
-    i8_pack<VEC>(x + v * VEC, r, o);
-    if constexpr (VEC == 1) p[k] = static_cast<int8_t>(o[0]);
-    else if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p + k) = make_uint2(o[0], o[1]);
-    else *reinterpret_cast<uint32_t *>(p + k) = o[0];
+  for (int v = 0; v < E / (VEC > 1 ? VEC : 2); ++v) {
+    uint32_t o[VEC > 1 ? VEC / 4 : 1];
+    if constexpr (VEC > 1) {
+      const int k = row_column<TEAM, VEC>(v * VEC);
+      if (k >= K) continue;
+      i8_pack<VEC / 2>(x + v * VEC / 2, r, o);
+      if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p + k) = make_uint2(o[0], o[1]);
+      else *reinterpret_cast<uint32_t *>(p + k) = o[0];
+    } else {
+      i8_pack<1>(x + v, r, o);
+      const int k0 = row_column<TEAM, 1>(2 * v), k1 = row_column<TEAM, 1>(2 * v + 1);
+      if (k0 < K) p[k0] = static_cast<int8_t>(o[0]);
+      if (k1 < K) p[k1] = static_cast<int8_t>(o[0] >> 8);
+    }
   }
 }
 
-// VEC parameters (of their own type, aligned to the vector's size where VEC > 1) from element `at` on.
-// They are read again for every row: the rows of a block, and of the SM's other blocks, find them in L1,
-// and the registers stay with the rows in flight.
-template <int VEC>
-__device__ __forceinline__ void load_params(const void *base, int dtype, size_t at, float (&w)[VEC]) {
-  if constexpr (VEC == 1) {
-    w[0] = dtype == SVDQ_F32   ? __ldg(static_cast<const float *>(base) + at)
-           : dtype == SVDQ_F16 ? to_f32(__ldg(static_cast<const __half *>(base) + at))
-                               : to_f32(__ldg(static_cast<const __nv_bfloat16 *>(base) + at));
-  } else if (dtype == SVDQ_F32) {
-    const float *p = static_cast<const float *>(base) + at;
+// x[i] = f(x[i]) for the pairs within the row; columns from K on keep their zeros.
+template <int TEAM, int VEC, int E, typename F>
+__device__ __forceinline__ void within_row(int K, f32x2 (&x)[E / 2], F f) {
+  if constexpr (VEC > 1) {
 #pragma unroll
-    for (int e = 0; e < VEC; e += 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4 *>(p + e));
-      w[e] = f.x, w[e + 1] = f.y, w[e + 2] = f.z, w[e + 3] = f.w;
+    for (int v = 0; v < E / VEC; ++v)
+      if (row_column<TEAM, VEC>(v * VEC) < K)
+#pragma unroll
+        for (int i = v * VEC / 2; i < (v + 1) * VEC / 2; ++i) x[i] = f(x[i], i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const f32x2 y = f(x[i], i);
+      x[i] = pair(row_column<TEAM, VEC>(2 * i) < K ? lo(y) : 0.0f, row_column<TEAM, VEC>(2 * i + 1) < K ? hi(y) : 0.0f);
+    }
+  }
+}
+
+// A row of parameters (of its own type, aligned to a vector's size where VEC > 1) in the same columns: kept
+// in registers for all rows of a block.
+template <int TEAM, int VEC, int E>
+__device__ __forceinline__ void load_params(const void *base, int dtype, size_t at, int K, float add, f32x2 (&w)[E / 2]) {
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k = row_column<TEAM, VEC>(2 * i + e);
+        f[e] = k >= K               ? 0.0f
+               : dtype == SVDQ_F32 ? add + static_cast<const float *>(base)[at + k]
+               : dtype == SVDQ_F16 ? add + to_f32(static_cast<const __half *>(base)[at + k])
+                                   : add + to_f32(static_cast<const __nv_bfloat16 *>(base)[at + k]);
+      }
+      w[i] = pair(f[0], f[1]);
     }
   } else {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-    uint32_t q[VEC / 2];
-    if constexpr (VEC == 8) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-      q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
-    } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-      q[0] = u.x, q[1] = u.y;
-    }
+    const f32x2 add_both = both(add);
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      if (dtype == SVDQ_F16) unpack2(q[e], w[2 * e], w[2 * e + 1], __half{});
-      else unpack2(q[e], w[2 * e], w[2 * e + 1], __nv_bfloat16{});
+    for (int v = 0; v < E / VEC; ++v) {
+      const int k = row_column<TEAM, VEC>(v * VEC);
+      f32x2 *to = w + v * VEC / 2;
+      if (k >= K) {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) to[e] = 0;
+      } else if (dtype == SVDQ_F32) {
+        const float *p = static_cast<const float *>(base) + at + k;
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(p + e);
+          to[e / 2] = add2(pair(f.x, f.y), add_both);
+          to[e / 2 + 1] = add2(pair(f.z, f.w), add_both);
+        }
+      } else {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at + k;
+        uint32_t q[VEC / 2];
+        if constexpr (VEC == 8) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(p);
+          q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(p);
+          q[0] = u.x, q[1] = u.y;
+        }
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e)
+          to[e] = add2(dtype == SVDQ_F16 ? widen(q[e], __half{}) : widen(q[e], __nv_bfloat16{}), add_both);
+      }
     }
   }
 }
 
-// f(i, parameter) for every value i of the thread that exists.
-template <int TEAM, int VEC, int E, typename F>
-__device__ __forceinline__ void with_params(const void *base, int dtype, size_t at, int K, F f) {
-#pragma unroll
-  for (int v = 0; v < E / VEC; ++v) {
-    const int k = row_column<TEAM, VEC>(v * VEC);
-    if (k >= K) continue;
-    float w[VEC];
-    load_params<VEC>(base, dtype, at + k, w);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) f(v * VEC + e, w[e]);
-  }
-}
-
-// Rows fetched ahead of the present one: two of 16-bit types, one of fp32 (the same registers).
-template <typename T, int TEAM, int VEC, int E>
+// Rows fetched ahead of the present one.
+template <typename T, int TEAM, int VEC, int E, int DEPTH>
 struct RowsAhead {
-  static constexpr int DEPTH = sizeof(T) == 2 && VEC > 1 ? 2 : 1;
   RawRow<T, TEAM, VEC, E> row[DEPTH];
 
   __device__ __forceinline__ void start(const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
@@ -171,19 +197,52 @@ struct RowsAhead {
       if (m0 + d < m1) row[d].load(x0 + (m0 + d) * stride, K);
   }
   // row m's values; fetches row m + DEPTH
-  __device__ __forceinline__ void take(const T *x0, size_t stride, int64_t m, int64_t m1, int K, float (&x)[E]) {
+  __device__ __forceinline__ void take(const T *x0, size_t stride, int64_t m, int64_t m1, int K, f32x2 (&x)[E / 2]) {
     row[0].values(x);
-    if constexpr (DEPTH == 2) row[0] = row[1];
+#pragma unroll
+    for (int d = 0; d + 1 < DEPTH; ++d) row[d] = row[d + 1];
     if (m + DEPTH < m1) row[DEPTH - 1].load(x0 + (m + DEPTH) * stride, K);
   }
 };
+
+// A thread's sums, in four chains.
+template <int N>
+__device__ __forceinline__ float thread_sum(const f32x2 (&x)[N]) {
+  f32x2 s = x[0], t = x[1];
+#pragma unroll
+  for (int i = 2; i < N; i += 2) {
+    s = add2(s, x[i]);
+    t = add2(t, x[i + 1]);
+  }
+  s = add2(s, t);
+  return lo(s) + hi(s);
+}
+template <int N>
+__device__ __forceinline__ float thread_dot(const f32x2 (&x)[N], const f32x2 (&y)[N]) {
+  f32x2 s = mul2(x[0], y[0]), t = mul2(x[1], y[1]);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) {
+    s = fma2(x[i], y[i], s);
+    t = fma2(x[i + 1], y[i + 1], t);
+  }
+  s = add2(s, t);
+  return lo(s) + hi(s);
+}
+// Bits of the largest |x|, infinities and NaNs above all others.
+template <int N>
+__device__ __forceinline__ uint32_t thread_top(const f32x2 (&x)[N]) {
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) t = max_abs3(t, lo(x[i]), hi(x[i]));
+  return __float_as_uint(t);
+}
 
 // Sums of N values over the block, in every thread and in a fixed order. Consecutive reductions use the
 // two buffers in turn (turn is the caller's count), so one barrier each is enough.
 template <int TEAM, int N>
 struct BlockSum {
   static constexpr int WARPS = TEAM / 32;
-  float part[2][WARPS][N];
+  alignas(16) float part[2][N][WARPS];
 
   __device__ __forceinline__ void operator()(float (&v)[N], uint32_t &turn) {
 #pragma unroll
@@ -191,17 +250,25 @@ struct BlockSum {
 #pragma unroll
       for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
     if constexpr (WARPS > 1) {
-      float(*p)[N] = part[turn++ & 1];
+      float(*p)[WARPS] = part[turn++ & 1];
       if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int n = 0; n < N; ++n) p[threadIdx.x >> 5][n] = v[n];
+        for (int n = 0; n < N; ++n) p[n][threadIdx.x >> 5] = v[n];
       __syncthreads();
 #pragma unroll
-      for (int n = 0; n < N; ++n) v[n] = 0.0f;
+      for (int n = 0; n < N; ++n) {
+        v[n] = 0.0f;
+        if constexpr (WARPS % 4 == 0) {
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w)
+          for (int w = 0; w < WARPS; w += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(p[n] + w);
+            v[n] += (f.x + f.y) + (f.z + f.w);
+          }
+        } else {
 #pragma unroll
-        for (int n = 0; n < N; ++n) v[n] += p[w][n];
+          for (int w = 0; w < WARPS; ++w) v[n] += p[n][w];
+        }
+      }
     }
   }
 };
@@ -240,9 +307,11 @@ auto for_row(int K, F f) {
 }
 constexpr int kMaxRow = 16384;
 
-// Blocks an SM holds at most: 1024 threads of 64 registers, at most 16 blocks.
-template <int TEAM>
-constexpr int kBlocksPerSm = TEAM >= 1024 ? 1 : (1024 / TEAM > 16 ? 16 : 1024 / TEAM);
+// Blocks of TEAM threads that hold about `threads` on an SM (at most 16 blocks).
+constexpr int blocks_per_sm(int team, int threads) {
+  const int b = threads / team;
+  return b < 1 ? 1 : (b > 16 ? 16 : b);
+}
 
 inline bool rows_aligned(const void *p, size_t stride, size_t elem, size_t to) {
   return reinterpret_cast<uintptr_t>(p) % to == 0 && stride * elem % to == 0;
