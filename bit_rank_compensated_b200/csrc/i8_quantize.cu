@@ -8,33 +8,38 @@
 namespace svdq {
 namespace {
 
-// Registers for the row, its smoothing and two rows ahead.
-template <int TEAM>
-constexpr int kBlocks = blocks_per_sm(TEAM, 1024);
+// Threads on an SM: registers for the row, its smoothing and two rows ahead.
+constexpr int kQuantThreads = 1024;
 
-template <typename T, int TEAM, int E, int VEC>
-__global__ void __launch_bounds__(TEAM, kBlocks<TEAM>) k_quantize_rows(QuantRowsLaunch a, int rows_per_block) {
+template <typename T, int TEAM, int E, int VEC, bool FULL>
+__global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_quantize_rows(QuantRowsLaunch a, int rows_per_block) {
   __shared__ BlockMax<TEAM> top;
+  top.clear();
   grid_dep_wait();
   grid_dep_launch();
   uint32_t turn = 0;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  RowsAhead<T, TEAM, VEC, E, (sizeof(T) == 2 && VEC > 1) ? 2 : 1> ahead;
+  constexpr int AHEAD = sizeof(T) == 2 && VEC > 1 ? 2 : 1;
+  RowsAhead<T, TEAM, VEC, E, FULL, AHEAD> ahead;
   ahead.start(x0, a.x_stride, m0, m1, a.K);
   f32x2 c[E / 2];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) c[i] = both(1.0f);  // exact
-  if (a.col_scale) load_params<TEAM, VEC, E>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
-  for (int64_t m = m0; m < m1; ++m) {
+  if (a.col_scale) load_params<TEAM, VEC, E, FULL>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
+  auto one_row = [&](int64_t m, int slot) {
     f32x2 x[E / 2];
-    ahead.take(x0, a.x_stride, m, m1, a.K, x);
+    ahead.take(slot, x0, a.x_stride, m, m1, a.K, x);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c[i]);
     const RowScale r = row_scale(top(thread_top(x), turn));
     if (threadIdx.x == 0) a.x_scale[m] = r.scale;
-    store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
+    store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
+  };
+  for (int64_t m = m0; m < m1; m += AHEAD) {
+    one_row(m, 0);
+    if (AHEAD > 1 && m + 1 < m1) one_row(m + 1, AHEAD - 1);
   }
 }
 
@@ -61,11 +66,14 @@ cudaError_t quantize_t(const QuantRowsLaunch &a) {
   const bool vec = a.K % kVec<T> == 0 && rows_aligned(a.X, a.M > 1 ? a.x_stride : 0, sizeof(T), 16) &&
                    rows_aligned(a.col_scale, 0, 4, 16);
   return for_row(a.K, [&]<int TEAM, int E>() {
-    const int blocks = a.num_sms * kBlocks<TEAM>;
+    const int threads = row_threads(a.K, E);
+    const int blocks = a.num_sms * blocks_per_sm(threads, kQuantThreads);
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
-    if (vec) return launch_dependent(k_quantize_rows<T, TEAM, E, kVec<T>>, grid, TEAM, 0, a.stream, a, rows);
-    return launch_dependent(k_quantize_rows<T, TEAM, E, 1>, grid, TEAM, 0, a.stream, a, rows);
+    auto kern = !vec                 ? k_quantize_rows<T, TEAM, E, 1, false>
+                : row_full(a.K, E) ? k_quantize_rows<T, TEAM, E, kVec<T>, true>
+                                   : k_quantize_rows<T, TEAM, E, kVec<T>, false>;
+    return launch_dependent(kern, grid, threads, 0, a.stream, a, rows);
   });
 }
 

@@ -23,22 +23,25 @@ namespace {
 // Threads on an SM: registers for the row, its weight and bias and two rows ahead; a row of 1024
 // threads has too few registers for that and reads its weights again for every row (from L1).
 template <int TEAM>
-constexpr int kForwardBlocks = blocks_per_sm(TEAM, 768);
+constexpr int kForwardThreads = TEAM < 1024 ? 768 : 1024;
 template <int TEAM>
 constexpr bool kKeepParams = TEAM < 1024;
 
 // Forward: rows [block's first, last) of X; QUANT writes int8 rows and their scales instead of Y.
-template <typename T, int TEAM, int E, int VEC, bool QUANT>
-__global__ void __launch_bounds__(TEAM, kForwardBlocks<TEAM>) k_layer_norm(NormLaunch a, int rows_per_block) {
+template <typename T, int TEAM, int E, int VEC, bool FULL, bool QUANT>
+__global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM>)) k_layer_norm(NormLaunch a, int rows_per_block) {
   __shared__ BlockSum<TEAM, 1> sum;
   __shared__ BlockMax<TEAM> top;
+  sum.clear();
+  if (QUANT) top.clear();
   grid_dep_wait();
   grid_dep_launch();
   uint32_t turn = 0, tmax = 0;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  RowsAhead<T, TEAM, VEC, E, (sizeof(T) == 2 && VEC > 1 && TEAM < 1024) ? 2 : 1> ahead;
+  constexpr int AHEAD = sizeof(T) == 2 && VEC > 1 && TEAM < 1024 ? 2 : 1;
+  RowsAhead<T, TEAM, VEC, E, FULL, AHEAD> ahead;
   ahead.start(x0, a.x_stride, m0, m1, a.K);
   f32x2 w[E / 2], b[E / 2];
 #pragma unroll
@@ -48,23 +51,23 @@ __global__ void __launch_bounds__(TEAM, kForwardBlocks<TEAM>) k_layer_norm(NormL
   }
   int64_t group_end = m0;  // first row of the next group
   const float inv_k = 1.0f / a.K;
-  for (int64_t m = m0; m < m1; ++m) {
+  auto one_row = [&](int64_t m, int slot) {
     f32x2 x[E / 2];
-    ahead.take(x0, a.x_stride, m, m1, a.K, x);
+    ahead.take(slot, x0, a.x_stride, m, m1, a.K, x);
     if (m >= group_end || !kKeepParams<TEAM>) {
       const size_t group = static_cast<uint32_t>(m) / static_cast<uint32_t>(a.rows_per_group);
       group_end = static_cast<int64_t>(group + 1) * a.rows_per_group;
-      if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
-      if (a.bias) load_params<TEAM, VEC, E>(a.bias, a.param_dtype, group * a.bias_stride, a.K, 0.0f, b);
+      if (a.weight) load_params<TEAM, VEC, E, FULL>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
+      if (a.bias) load_params<TEAM, VEC, E, FULL>(a.bias, a.param_dtype, group * a.bias_stride, a.K, 0.0f, b);
     }
     float v[1] = {thread_sum(x)};
     sum(v, turn);
     const float mean = v[0] * inv_k;
     const f32x2 minus = both(-mean);
-    within_row<TEAM, VEC, E>(a.K, x, [&](f32x2 p, int) { return add2(p, minus); });
+    within_row<TEAM, VEC, E, FULL>(a.K, x, [&](f32x2 p, int) { return add2(p, minus); });
     v[0] = thread_dot(x, x);
     sum(v, turn);
-    const float rstd = 1.0f / sqrtf(fmaf(v[0], inv_k, a.eps));
+    const float rstd = rsqrtf(fmaf(v[0], inv_k, a.eps));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[m] = mean;
       if (a.rstd) a.rstd[m] = rstd;
@@ -73,25 +76,29 @@ __global__ void __launch_bounds__(TEAM, kForwardBlocks<TEAM>) k_layer_norm(NormL
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) x[i] = fma2(mul2(x[i], r2), w[i], b[i]);
     if constexpr (!QUANT) {
-      store_row<T, TEAM, VEC, E>(static_cast<T *>(a.Y) + m * a.y_stride, a.K, x);
+      store_row<T, TEAM, VEC, E, FULL>(static_cast<T *>(a.Y) + m * a.y_stride, a.K, x);
     } else {
       // columns from K on are zeros still: their x and b are
       const RowScale r = row_scale(top(thread_top(x), tmax));
       if (threadIdx.x == 0) a.x_scale[m] = r.scale;
-      store_codes<TEAM, VEC, E>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
+      store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
     }
+  };
+  for (int64_t m = m0; m < m1; m += AHEAD) {
+    one_row(m, 0);
+    if (AHEAD > 1 && m + 1 < m1) one_row(m + 1, AHEAD - 1);
   }
 }
 
 // Gradient: block (group g, slice s) takes rows [chunk s of the group]. Partial sums go to
 // partial[block][2][K], or straight to dweight and dbias where a group has one slice.
-template <int TEAM>
-constexpr int kBackwardBlocks = blocks_per_sm(TEAM, 512);
+constexpr int kBackwardThreads = 512;
 
-template <typename T, int TEAM, int E, int VEC>
-__global__ void __launch_bounds__(TEAM, kBackwardBlocks<TEAM>) k_layer_norm_backward(NormLaunch a, int slices, int chunk) {
+template <typename T, int TEAM, int E, int VEC, bool FULL>
+__global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k_layer_norm_backward(NormLaunch a, int slices, int chunk) {
   __shared__ BlockSum<TEAM, 2> sum;
   grid_dep_launch();
+  sum.clear();
   uint32_t turn = 0;
   const int group = blockIdx.x / slices, slice = blockIdx.x % slices;
   const int64_t g0 = static_cast<int64_t>(group) * a.rows_per_group;
@@ -100,7 +107,7 @@ __global__ void __launch_bounds__(TEAM, kBackwardBlocks<TEAM>) k_layer_norm_back
   const int64_t m1 = m0 + chunk < g1 ? m0 + chunk : g1;
   if (m0 >= m1) return;
   const T *x0 = static_cast<const T *>(a.X), *dy0 = static_cast<const T *>(a.dY);
-  RowsAhead<T, TEAM, VEC, E, 1> xs, ds;
+  RowsAhead<T, TEAM, VEC, E, FULL, 1> xs, ds;
   xs.start(x0, a.x_stride, m0, m1, a.K);
   ds.start(dy0, a.dy_stride, m0, m1, a.K);
   float mean_n = a.mean[m0], rstd_n = a.rstd[m0];
@@ -110,12 +117,12 @@ __global__ void __launch_bounds__(TEAM, kBackwardBlocks<TEAM>) k_layer_norm_back
     dw[i] = db[i] = 0;
     w[i] = both(1.0f);
   }
-  if (a.weight) load_params<TEAM, VEC, E>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
+  if (a.weight) load_params<TEAM, VEC, E, FULL>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
   const float inv_k = 1.0f / a.K;
   for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2], g[E / 2];
-    xs.take(x0, a.x_stride, m, m1, a.K, x);
-    ds.take(dy0, a.dy_stride, m, m1, a.K, g);
+    xs.take(0, x0, a.x_stride, m, m1, a.K, x);
+    ds.take(0, dy0, a.dy_stride, m, m1, a.K, g);
     const f32x2 minus = both(-mean_n), r2 = both(rstd_n);
     const float rstd = rstd_n;
     if (m + 1 < m1) {
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(TEAM, kBackwardBlocks<TEAM>) k_layer_norm_back
       const f32x2 c0 = both(-v[0] * inv_k * rstd), c1 = both(-v[1] * inv_k * rstd);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) x[i] = fma2(g[i], r2, fma2(x[i], c1, c0));
-      store_row<T, TEAM, VEC, E>(static_cast<T *>(a.dX) + m * a.dx_stride, a.K, x);
+      store_row<T, TEAM, VEC, E, FULL>(static_cast<T *>(a.dX) + m * a.dx_stride, a.K, x);
     }
   }
   if (!a.dweight && !a.dbias) return;
@@ -145,7 +152,7 @@ __global__ void __launch_bounds__(TEAM, kBackwardBlocks<TEAM>) k_layer_norm_back
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int k = row_column<TEAM, VEC>(i);
-    if (k < a.K) {
+    if (FULL || k < a.K) {
       if (pw) pw[at + k] = i % 2 ? hi(dw[i / 2]) : lo(dw[i / 2]);
       if (pb) pb[at + k] = i % 2 ? hi(db[i / 2]) : lo(db[i / 2]);
     }
@@ -198,11 +205,14 @@ template <typename T, bool QUANT>
 cudaError_t forward_t(const NormLaunch &a) {
   return for_row(a.K, [&]<int TEAM, int E>() {
     // a block's rows are consecutive: as many blocks as are resident at once
-    const int blocks = a.num_sms * kForwardBlocks<TEAM>;
+    const int threads = row_threads(a.K, E);
+    const int blocks = a.num_sms * blocks_per_sm(threads, kForwardThreads<TEAM>);
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
-    if (vectors<T>(a)) return launch_dependent(k_layer_norm<T, TEAM, E, kVec<T>, QUANT>, grid, TEAM, 0, a.stream, a, rows);
-    return launch_dependent(k_layer_norm<T, TEAM, E, 1, QUANT>, grid, TEAM, 0, a.stream, a, rows);
+    auto kern = !vectors<T>(a)       ? k_layer_norm<T, TEAM, E, 1, false, QUANT>
+                : row_full(a.K, E) ? k_layer_norm<T, TEAM, E, kVec<T>, true, QUANT>
+                                   : k_layer_norm<T, TEAM, E, kVec<T>, false, QUANT>;
+    return launch_dependent(kern, grid, threads, 0, a.stream, a, rows);
   });
 }
 
@@ -222,7 +232,7 @@ struct Slices {
 Slices slices_of(int M, int K, int rows_per_group) {
   const int used = (M + rows_per_group - 1) / rows_per_group;
   const int rows = M < rows_per_group ? M : rows_per_group;
-  const int blocks = 148 * for_row(K, []<int TEAM, int>() { return kBackwardBlocks<TEAM>; });
+  const int blocks = 148 * blocks_per_sm(row_threads(K, K <= 256 ? 8 : 16), kBackwardThreads);
   int s = blocks / used;
   if (s > (rows + 3) / 4) s = (rows + 3) / 4;
   if (s < 1) s = 1;
@@ -243,8 +253,10 @@ cudaError_t backward_t(const NormLaunch &a) {
   }
   const cudaError_t e = for_row(a.K, [&]<int TEAM, int E>() {
     const dim3 grid(static_cast<unsigned>(used) * s.slices);
-    if (vectors<T>(a)) k_layer_norm_backward<T, TEAM, E, kVec<T>><<<grid, TEAM, 0, a.stream>>>(a, s.slices, s.chunk);
-    else k_layer_norm_backward<T, TEAM, E, 1><<<grid, TEAM, 0, a.stream>>>(a, s.slices, s.chunk);
+    auto kern = !vectors<T>(a)       ? k_layer_norm_backward<T, TEAM, E, 1, false>
+                : row_full(a.K, E) ? k_layer_norm_backward<T, TEAM, E, kVec<T>, true>
+                                   : k_layer_norm_backward<T, TEAM, E, kVec<T>, false>;
+    kern<<<grid, row_threads(a.K, E), 0, a.stream>>>(a, s.slices, s.chunk);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !sums || s.slices == 1) return e;

@@ -1,9 +1,11 @@
 // A row spread over the threads of a block, in registers: what the layer norm's kernels and the row
 // quantizer share.
 //
-// Thread t of TEAM holds E values as E / 2 pairs: VEC consecutive ones at columns (v TEAM + t) VEC, v = 0 ..
-// E / VEC - 1, VEC values being 16 bytes (one load), or VEC = 1 where rows do not start on 16 bytes or
-// do not end on a whole vector (consecutive threads on consecutive columns). Columns from K on hold zeros.
+// Thread t of a block of T <= TEAM threads holds E values as E / 2 pairs: VEC consecutive ones at columns
+// (v T + t) VEC, v = 0 .. E / VEC - 1, VEC values being 16 bytes (one load), or VEC = 1 where rows do not
+// start on 16 bytes or do not end on a whole vector (consecutive threads on consecutive columns). T is
+// the row's length over E, in whole warps; where that leaves nothing over (FULL), no column is checked.
+// Else columns from K on hold zeros.
 #pragma once
 
 #include <stdint.h>
@@ -20,7 +22,8 @@ constexpr int kVec = 16 / sizeof(T);
 
 template <int TEAM, int VEC>
 __device__ __forceinline__ int row_column(int i) {
-  return ((i / VEC) * TEAM + static_cast<int>(threadIdx.x)) * VEC + i % VEC;
+  const int t = TEAM == 32 ? 32 : static_cast<int>(blockDim.x);
+  return ((i / VEC) * t + static_cast<int>(threadIdx.x)) * VEC + i % VEC;
 }
 
 // Two 16-bit values of a word as fp32, and back.
@@ -39,7 +42,7 @@ __device__ __forceinline__ uint32_t narrow(f32x2 v, __half) {
 }
 
 // A row's values as loaded (so that a row fetched ahead takes half the registers of its fp32 values).
-template <typename T, int TEAM, int VEC, int E>
+template <typename T, int TEAM, int VEC, int E, bool FULL>
 struct RawRow {
   static constexpr int WORDS = VEC > 1 ? E * static_cast<int>(sizeof(T)) / 4 : E;
   uint32_t w[WORDS];
@@ -49,7 +52,7 @@ struct RawRow {
 #pragma unroll
       for (int v = 0; v < E / VEC; ++v) {
         const int k = row_column<TEAM, VEC>(v * VEC);
-        const uint4 q = k < K ? *reinterpret_cast<const uint4 *>(p + k) : make_uint4(0, 0, 0, 0);
+        const uint4 q = FULL || k < K ? *reinterpret_cast<const uint4 *>(p + k) : make_uint4(0, 0, 0, 0);
         w[4 * v] = q.x;
         w[4 * v + 1] = q.y;
         w[4 * v + 2] = q.z;
@@ -59,7 +62,7 @@ struct RawRow {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int k = row_column<TEAM, VEC>(i);
-        w[i] = k < K ? __float_as_uint(to_f32(p[k])) : 0u;
+        w[i] = FULL || k < K ? __float_as_uint(to_f32(p[k])) : 0u;
       }
     }
   }
@@ -72,19 +75,19 @@ struct RawRow {
   }
 };
 
-template <typename T, int TEAM, int VEC, int E>
+template <typename T, int TEAM, int VEC, int E, bool FULL>
 __device__ __forceinline__ void store_row(T *p, int K, const f32x2 (&y)[E / 2]) {
   if constexpr (VEC == 1) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int k = row_column<TEAM, VEC>(i);
-      if (k < K) p[k] = from_f32<T>(i % 2 ? hi(y[i / 2]) : lo(y[i / 2]));
+      if (FULL || k < K) p[k] = from_f32<T>(i % 2 ? hi(y[i / 2]) : lo(y[i / 2]));
     }
   } else {
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v) {
       const int k = row_column<TEAM, VEC>(v * VEC);
-      if (k >= K) continue;
+      if (!FULL && k >= K) continue;
       const f32x2 *s = y + v * VEC / 2;
       uint4 o;
       if constexpr (sizeof(T) == 4) o = make_uint4(lo_bits(s[0]), hi_bits(s[0]), lo_bits(s[1]), hi_bits(s[1]));
@@ -95,47 +98,47 @@ __device__ __forceinline__ void store_row(T *p, int K, const f32x2 (&y)[E / 2]) 
 }
 
 // The int8 codes of a row, VEC bytes a store, each vector as soon as it is formed.
-template <int TEAM, int VEC, int E>
+template <int TEAM, int VEC, int E, bool FULL>
 __device__ __forceinline__ void store_codes(int8_t *p, int K, const f32x2 (&x)[E / 2], const RowScale &r) {
 #pragma unroll
   for (int v = 0; v < E / (VEC > 1 ? VEC : 2); ++v) {
     uint32_t o[VEC > 1 ? VEC / 4 : 1];
     if constexpr (VEC > 1) {
       const int k = row_column<TEAM, VEC>(v * VEC);
-      if (k >= K) continue;
+      if (!FULL && k >= K) continue;
       i8_pack<VEC / 2>(x + v * VEC / 2, r, o);
       if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p + k) = make_uint2(o[0], o[1]);
       else *reinterpret_cast<uint32_t *>(p + k) = o[0];
     } else {
       i8_pack<1>(x + v, r, o);
       const int k0 = row_column<TEAM, 1>(2 * v), k1 = row_column<TEAM, 1>(2 * v + 1);
-      if (k0 < K) p[k0] = static_cast<int8_t>(o[0]);
-      if (k1 < K) p[k1] = static_cast<int8_t>(o[0] >> 8);
+      if (FULL || k0 < K) p[k0] = static_cast<int8_t>(o[0]);
+      if (FULL || k1 < K) p[k1] = static_cast<int8_t>(o[0] >> 8);
     }
   }
 }
 
 // x[i] = f(x[i]) for the pairs within the row; columns from K on keep their zeros.
-template <int TEAM, int VEC, int E, typename F>
+template <int TEAM, int VEC, int E, bool FULL, typename F>
 __device__ __forceinline__ void within_row(int K, f32x2 (&x)[E / 2], F f) {
   if constexpr (VEC > 1) {
 #pragma unroll
     for (int v = 0; v < E / VEC; ++v)
-      if (row_column<TEAM, VEC>(v * VEC) < K)
+      if (FULL || row_column<TEAM, VEC>(v * VEC) < K)
 #pragma unroll
         for (int i = v * VEC / 2; i < (v + 1) * VEC / 2; ++i) x[i] = f(x[i], i);
   } else {
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
       const f32x2 y = f(x[i], i);
-      x[i] = pair(row_column<TEAM, VEC>(2 * i) < K ? lo(y) : 0.0f, row_column<TEAM, VEC>(2 * i + 1) < K ? hi(y) : 0.0f);
+      x[i] = pair(FULL || row_column<TEAM, VEC>(2 * i) < K ? lo(y) : 0.0f, FULL || row_column<TEAM, VEC>(2 * i + 1) < K ? hi(y) : 0.0f);
     }
   }
 }
 
 // A row of parameters (of its own type, aligned to a vector's size where VEC > 1) in the same columns: kept
 // in registers for all rows of a block.
-template <int TEAM, int VEC, int E>
+template <int TEAM, int VEC, int E, bool FULL>
 __device__ __forceinline__ void load_params(const void *base, int dtype, size_t at, int K, float add, f32x2 (&w)[E / 2]) {
   if constexpr (VEC == 1) {
 #pragma unroll
@@ -144,7 +147,7 @@ __device__ __forceinline__ void load_params(const void *base, int dtype, size_t 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int k = row_column<TEAM, VEC>(2 * i + e);
-        f[e] = k >= K               ? 0.0f
+        f[e] = !FULL && k >= K      ? 0.0f
                : dtype == SVDQ_F32 ? add + static_cast<const float *>(base)[at + k]
                : dtype == SVDQ_F16 ? add + to_f32(static_cast<const __half *>(base)[at + k])
                                    : add + to_f32(static_cast<const __nv_bfloat16 *>(base)[at + k]);
@@ -157,7 +160,7 @@ __device__ __forceinline__ void load_params(const void *base, int dtype, size_t 
     for (int v = 0; v < E / VEC; ++v) {
       const int k = row_column<TEAM, VEC>(v * VEC);
       f32x2 *to = w + v * VEC / 2;
-      if (k >= K) {
+      if (!FULL && k >= K) {
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e) to[e] = 0;
       } else if (dtype == SVDQ_F32) {
@@ -186,22 +189,20 @@ __device__ __forceinline__ void load_params(const void *base, int dtype, size_t 
   }
 }
 
-// Rows fetched ahead of the present one.
-template <typename T, int TEAM, int VEC, int E, int DEPTH>
+// Rows fetched ahead of the present one: row m is in slot m mod DEPTH (counted from the block's first row).
+template <typename T, int TEAM, int VEC, int E, bool FULL, int DEPTH>
 struct RowsAhead {
-  RawRow<T, TEAM, VEC, E> row[DEPTH];
+  RawRow<T, TEAM, VEC, E, FULL> row[DEPTH];
 
   __device__ __forceinline__ void start(const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
       if (m0 + d < m1) row[d].load(x0 + (m0 + d) * stride, K);
   }
-  // row m's values; fetches row m + DEPTH
-  __device__ __forceinline__ void take(const T *x0, size_t stride, int64_t m, int64_t m1, int K, f32x2 (&x)[E / 2]) {
-    row[0].values(x);
-#pragma unroll
-    for (int d = 0; d + 1 < DEPTH; ++d) row[d] = row[d + 1];
-    if (m + DEPTH < m1) row[DEPTH - 1].load(x0 + (m + DEPTH) * stride, K);
+  // row m's values; fetches row m + DEPTH into its slot
+  __device__ __forceinline__ void take(int slot, const T *x0, size_t stride, int64_t m, int64_t m1, int K, f32x2 (&x)[E / 2]) {
+    row[slot].values(x);
+    if (m + DEPTH < m1) row[slot].load(x0 + (m + DEPTH) * stride, K);
   }
 };
 
@@ -237,36 +238,49 @@ __device__ __forceinline__ uint32_t thread_top(const f32x2 (&x)[N]) {
   return __float_as_uint(t);
 }
 
-// Sums of N values over the block, in every thread and in a fixed order. Consecutive reductions use the
-// two buffers in turn (turn is the caller's count), so one barrier each is enough.
+// Sums over the block, in every thread and in a fixed order: of one value, or of two, which the halves of
+// a warp share out after their first exchange. Consecutive reductions use the two buffers in turn (turn
+// is the caller's count), so one barrier each is enough. Warps that a block does not have count as zeros.
 template <int TEAM, int N>
 struct BlockSum {
   static constexpr int WARPS = TEAM / 32;
+  static_assert(N == 1 || N == 2);
   alignas(16) float part[2][N][WARPS];
 
-  __device__ __forceinline__ void operator()(float (&v)[N], uint32_t &turn) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  __device__ __forceinline__ void clear() {
     if constexpr (WARPS > 1) {
-      float(*p)[WARPS] = part[turn++ & 1];
-      if ((threadIdx.x & 31) == 0)
+      for (int i = threadIdx.x; i < 2 * N * WARPS; i += blockDim.x) part[0][0][i] = 0.0f;
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ void operator()(float (&v)[N], uint32_t &turn) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (WARPS == 1) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) p[n][threadIdx.x >> 5] = v[n];
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    } else {
+      float s = v[0];
+      if constexpr (N == 2) {
+        const bool second = lane >= 16;
+        s = (second ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, second ? v[0] : v[1], 16);
+      } else {
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      float(*p)[WARPS] = part[turn++ & 1];
+      if (lane == 0) p[0][threadIdx.x >> 5] = s;
+      if (N == 2 && lane == 16) p[N - 1][threadIdx.x >> 5] = s;
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         v[n] = 0.0f;
-        if constexpr (WARPS % 4 == 0) {
 #pragma unroll
-          for (int w = 0; w < WARPS; w += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(p[n] + w);
-            v[n] += (f.x + f.y) + (f.z + f.w);
-          }
-        } else {
-#pragma unroll
-          for (int w = 0; w < WARPS; ++w) v[n] += p[n][w];
+        for (int w = 0; w < WARPS; w += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(p[n] + w);
+          v[n] += (f.x + f.y) + (f.z + f.w);
         }
       }
     }
@@ -277,8 +291,14 @@ struct BlockSum {
 template <int TEAM>
 struct BlockMax {
   static constexpr int WARPS = TEAM / 32;
-  uint32_t part[2][WARPS];
+  alignas(16) uint32_t part[2][WARPS];
 
+  __device__ __forceinline__ void clear() {
+    if constexpr (WARPS > 1) {
+      for (int i = threadIdx.x; i < 2 * WARPS; i += blockDim.x) part[0][i] = 0;
+      __syncthreads();
+    }
+  }
   __device__ __forceinline__ uint32_t operator()(uint32_t v, uint32_t &turn) {
     v = __reduce_max_sync(0xffffffffu, v);
     if constexpr (WARPS > 1) {
@@ -287,30 +307,35 @@ struct BlockMax {
       __syncthreads();
       v = 0;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) v = max(v, p[w]);
+      for (int w = 0; w < WARPS; w += 4) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p + w);
+        v = max(max(v, max(q.x, q.y)), max(q.z, q.w));
+      }
     }
     return v;
   }
 };
 
-// Calls f.operator()<TEAM, E>() with the block that holds a row of K values: 8 a thread up to 256
-// columns, else 16, so that every block of a row has 2 to 32 warps' loads in flight.
+// Calls f.operator()<TEAM, E>() with the kind of block that holds a row of K values: 8 a thread up to 256
+// columns, else 16.
 template <typename F>
 auto for_row(int K, F f) {
   if (K <= 256) return f.template operator()<32, 8>();
   if (K <= 512) return f.template operator()<32, 16>();
-  if (K <= 1024) return f.template operator()<64, 16>();
   if (K <= 2048) return f.template operator()<128, 16>();
   if (K <= 4096) return f.template operator()<256, 16>();
   if (K <= 8192) return f.template operator()<512, 16>();
   return f.template operator()<1024, 16>();
 }
+// Threads of a row's block, and whether they hold nothing but the row.
+inline int row_threads(int K, int E) { return ((K + E - 1) / E + 31) / 32 * 32; }
+inline bool row_full(int K, int E) { return K % (32 * E) == 0; }
 constexpr int kMaxRow = 16384;
 
-// Blocks of TEAM threads that hold about `threads` on an SM (at most 16 blocks).
+// Blocks of `team` threads that make about `threads` on an SM (at most 24 blocks).
 constexpr int blocks_per_sm(int team, int threads) {
   const int b = threads / team;
-  return b < 1 ? 1 : (b > 16 ? 16 : b);
+  return b < 1 ? 1 : (b > 24 ? 24 : b);
 }
 
 inline bool rows_aligned(const void *p, size_t stride, size_t elem, size_t to) {
