@@ -86,6 +86,13 @@ struct RopeLaunch {
 cudaError_t launch_rope_table(const RopeLaunch &a);
 cudaError_t launch_rope_apply(const RopeLaunch &a);
 
+// Lets a kernel have `bytes` of dynamic shared memory on the current device.
+template <typename... Args>
+cudaError_t allow_smem(void (*kern)(Args...), int bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;  // within the default, static arrays included
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // Launches a kernel that waits (grid_dep_wait) before it touches global memory, so that its start may
 // overlap the end of the stream's previous kernel.
 template <typename... Args>

@@ -8,7 +8,11 @@
 namespace svdq {
 namespace {
 
-// Threads on an SM: registers for the row, its smoothing and two rows ahead.
+// Rows in flight, and threads on an SM (registers for the row and its smoothing).
+template <typename T>
+constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+template <typename T, int TEAM, int VEC, int E, bool FULL>
+using Ahead = RowsAhead<T, TEAM, VEC, E, FULL, kDepth<T>>;
 constexpr int kQuantThreads = 1024;
 
 template <typename T, int TEAM, int E, int VEC, bool FULL>
@@ -21,25 +25,30 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  constexpr int AHEAD = sizeof(T) == 2 && VEC > 1 ? 2 : 1;
-  RowsAhead<T, TEAM, VEC, E, FULL, AHEAD> ahead;
-  ahead.start(x0, a.x_stride, m0, m1, a.K);
+  extern __shared__ __align__(16) uint8_t ring[];
+  Ahead<T, TEAM, VEC, E, FULL> ahead;
+#pragma unroll
+  for (int d = 0; d < kDepth<T>; ++d) {
+    ahead.start(ring, d, x0, a.x_stride, m0, m1, a.K);
+    copies_commit();
+  }
   f32x2 c[E / 2];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) c[i] = both(1.0f);  // exact
   if (a.col_scale) load_params<TEAM, VEC, E, FULL>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
-  auto one_row = [&](int64_t m, int slot) {
+  int slot = 0;
+  for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2];
-    ahead.take(slot, x0, a.x_stride, m, m1, a.K, x);
+    copies_wait<kDepth<T> - 1>();
+    ahead.take(slot, a.K, x);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c[i]);
     const RowScale r = row_scale(top(thread_top(x), turn));
+    ahead.refill(slot, x0, a.x_stride, m, m1, a.K);
+    copies_commit();
+    slot = slot + 1 == kDepth<T> ? 0 : slot + 1;
     if (threadIdx.x == 0) a.x_scale[m] = r.scale;
     store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
-  };
-  for (int64_t m = m0; m < m1; m += AHEAD) {
-    one_row(m, 0);
-    if (AHEAD > 1 && m + 1 < m1) one_row(m + 1, AHEAD - 1);
   }
 }
 
@@ -73,7 +82,9 @@ cudaError_t quantize_t(const QuantRowsLaunch &a) {
     auto kern = !vec                 ? k_quantize_rows<T, TEAM, E, 1, false>
                 : row_full(a.K, E) ? k_quantize_rows<T, TEAM, E, kVec<T>, true>
                                    : k_quantize_rows<T, TEAM, E, kVec<T>, false>;
-    return launch_dependent(kern, grid, threads, 0, a.stream, a, rows);
+    const int smem = vec ? Ahead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
+    const cudaError_t e = allow_smem(kern, smem);
+    return e != cudaSuccess ? e : launch_dependent(kern, grid, threads, smem, a.stream, a, rows);
   });
 }
 

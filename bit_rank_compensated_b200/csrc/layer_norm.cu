@@ -20,8 +20,14 @@
 namespace svdq {
 namespace {
 
-// Threads on an SM: registers for the row, its weight and bias and two rows ahead; a row of 1024
-// threads has too few registers for that and reads its weights again for every row (from L1).
+// Rows in flight.
+template <typename T>
+constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+template <typename T, int TEAM, int VEC, int E, bool FULL>
+using Ahead = RowsAhead<T, TEAM, VEC, E, FULL, kDepth<T>>;
+
+// Threads on an SM: registers for the row, its weight and bias; a row of 1024 threads has too few for
+// that and reads its weights again for every row (from L1).
 template <int TEAM>
 constexpr int kForwardThreads = TEAM < 1024 ? 768 : 1024;
 template <int TEAM>
@@ -40,9 +46,13 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
   const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
   const T *x0 = static_cast<const T *>(a.X);
-  constexpr int AHEAD = sizeof(T) == 2 && VEC > 1 && TEAM < 1024 ? 2 : 1;
-  RowsAhead<T, TEAM, VEC, E, FULL, AHEAD> ahead;
-  ahead.start(x0, a.x_stride, m0, m1, a.K);
+  extern __shared__ __align__(16) uint8_t ring[];
+  Ahead<T, TEAM, VEC, E, FULL> ahead;
+#pragma unroll
+  for (int d = 0; d < kDepth<T>; ++d) {
+    ahead.start(ring, d, x0, a.x_stride, m0, m1, a.K);
+    copies_commit();
+  }
   f32x2 w[E / 2], b[E / 2];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) {
@@ -51,9 +61,11 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
   }
   int64_t group_end = m0;  // first row of the next group
   const float inv_k = 1.0f / a.K;
-  auto one_row = [&](int64_t m, int slot) {
+  int slot = 0;
+  for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2];
-    ahead.take(slot, x0, a.x_stride, m, m1, a.K, x);
+    copies_wait<kDepth<T> - 1>();
+    ahead.take(slot, a.K, x);
     if (m >= group_end || !kKeepParams<TEAM>) {
       const size_t group = static_cast<uint32_t>(m) / static_cast<uint32_t>(a.rows_per_group);
       group_end = static_cast<int64_t>(group + 1) * a.rows_per_group;
@@ -62,6 +74,9 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
     }
     float v[1] = {thread_sum(x)};
     sum(v, turn);
+    ahead.refill(slot, x0, a.x_stride, m, m1, a.K);
+    copies_commit();
+    slot = slot + 1 == kDepth<T> ? 0 : slot + 1;
     const float mean = v[0] * inv_k;
     const f32x2 minus = both(-mean);
     within_row<TEAM, VEC, E, FULL>(a.K, x, [&](f32x2 p, int) { return add2(p, minus); });
@@ -83,16 +98,17 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
       if (threadIdx.x == 0) a.x_scale[m] = r.scale;
       store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
     }
-  };
-  for (int64_t m = m0; m < m1; m += AHEAD) {
-    one_row(m, 0);
-    if (AHEAD > 1 && m + 1 < m1) one_row(m + 1, AHEAD - 1);
   }
 }
 
 // Gradient: block (group g, slice s) takes rows [chunk s of the group]. Partial sums go to
 // partial[block][2][K], or straight to dweight and dbias where a group has one slice.
 constexpr int kBackwardThreads = 512;
+// Rows of x and dy in flight (16384 fp32 values of each are 128 KiB).
+template <typename T, int TEAM>
+constexpr int kBackwardDepth = sizeof(T) == 2 ? 3 : (TEAM < 1024 ? 2 : 1);
+template <typename T, int TEAM, int VEC, int E, bool FULL>
+using BackwardAhead = RowsAhead<T, TEAM, VEC, E, FULL, kBackwardDepth<T, TEAM>>;
 
 template <typename T, int TEAM, int E, int VEC, bool FULL>
 __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k_layer_norm_backward(NormLaunch a, int slices, int chunk) {
@@ -107,9 +123,14 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k
   const int64_t m1 = m0 + chunk < g1 ? m0 + chunk : g1;
   if (m0 >= m1) return;
   const T *x0 = static_cast<const T *>(a.X), *dy0 = static_cast<const T *>(a.dY);
-  RowsAhead<T, TEAM, VEC, E, FULL, 1> xs, ds;
-  xs.start(x0, a.x_stride, m0, m1, a.K);
-  ds.start(dy0, a.dy_stride, m0, m1, a.K);
+  extern __shared__ __align__(16) uint8_t ring[];
+  BackwardAhead<T, TEAM, VEC, E, FULL> xs, ds;
+#pragma unroll
+  for (int d = 0; d < kBackwardDepth<T, TEAM>; ++d) {
+    xs.start(ring, d, x0, a.x_stride, m0, m1, a.K);
+    ds.start(ring + xs.bytes(blockDim.x), d, dy0, a.dy_stride, m0, m1, a.K);
+    copies_commit();
+  }
   float mean_n = a.mean[m0], rstd_n = a.rstd[m0];
   f32x2 w[E / 2], dw[E / 2], db[E / 2];
 #pragma unroll
@@ -119,10 +140,12 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k
   }
   if (a.weight) load_params<TEAM, VEC, E, FULL>(a.weight, a.param_dtype, group * a.weight_stride, a.K, a.weight_offset, w);
   const float inv_k = 1.0f / a.K;
+  int slot = 0;
   for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2], g[E / 2];
-    xs.take(0, x0, a.x_stride, m, m1, a.K, x);
-    ds.take(0, dy0, a.dy_stride, m, m1, a.K, g);
+    copies_wait<kBackwardDepth<T, TEAM> - 1>();
+    xs.take(slot, a.K, x);
+    ds.take(slot, a.K, g);
     const f32x2 minus = both(-mean_n), r2 = both(rstd_n);
     const float rstd = rstd_n;
     if (m + 1 < m1) {
@@ -136,6 +159,10 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k
       db[i] = add2(db[i], g[i]);
       g[i] = mul2(g[i], w[i]);
     }
+    xs.refill(slot, x0, a.x_stride, m, m1, a.K);
+    ds.refill(slot, dy0, a.dy_stride, m, m1, a.K);
+    copies_commit();
+    slot = slot + 1 == kBackwardDepth<T, TEAM> ? 0 : slot + 1;
     if (a.dX) {
       float v[2] = {thread_sum(g), thread_dot(g, x)};
       sum(v, turn);
@@ -209,10 +236,13 @@ cudaError_t forward_t(const NormLaunch &a) {
     const int blocks = a.num_sms * blocks_per_sm(threads, kForwardThreads<TEAM>);
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
-    auto kern = !vectors<T>(a)       ? k_layer_norm<T, TEAM, E, 1, false, QUANT>
+    const bool vec = vectors<T>(a);
+    const int smem = vec ? Ahead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
+    auto kern = !vec                 ? k_layer_norm<T, TEAM, E, 1, false, QUANT>
                 : row_full(a.K, E) ? k_layer_norm<T, TEAM, E, kVec<T>, true, QUANT>
                                    : k_layer_norm<T, TEAM, E, kVec<T>, false, QUANT>;
-    return launch_dependent(kern, grid, threads, 0, a.stream, a, rows);
+    const cudaError_t e = allow_smem(kern, smem);
+    return e != cudaSuccess ? e : launch_dependent(kern, grid, threads, smem, a.stream, a, rows);
   });
 }
 
@@ -253,10 +283,15 @@ cudaError_t backward_t(const NormLaunch &a) {
   }
   const cudaError_t e = for_row(a.K, [&]<int TEAM, int E>() {
     const dim3 grid(static_cast<unsigned>(used) * s.slices);
-    auto kern = !vectors<T>(a)       ? k_layer_norm_backward<T, TEAM, E, 1, false>
+    const bool vec = vectors<T>(a);
+    const int threads = row_threads(a.K, E);
+    const int smem = vec ? 2 * BackwardAhead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
+    auto kern = !vec                 ? k_layer_norm_backward<T, TEAM, E, 1, false>
                 : row_full(a.K, E) ? k_layer_norm_backward<T, TEAM, E, kVec<T>, true>
                                    : k_layer_norm_backward<T, TEAM, E, kVec<T>, false>;
-    kern<<<grid, row_threads(a.K, E), 0, a.stream>>>(a, s.slices, s.chunk);
+    const cudaError_t e = allow_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, threads, smem, a.stream>>>(a, s.slices, s.chunk);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !sums || s.slices == 1) return e;

@@ -41,40 +41,6 @@ __device__ __forceinline__ uint32_t narrow(f32x2 v, __half) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A row's values as loaded (so that a row fetched ahead takes half the registers of its fp32 values).
-template <typename T, int TEAM, int VEC, int E, bool FULL>
-struct RawRow {
-  static constexpr int WORDS = VEC > 1 ? E * static_cast<int>(sizeof(T)) / 4 : E;
-  uint32_t w[WORDS];
-
-  __device__ __forceinline__ void load(const T *p, int K) {
-    if constexpr (VEC > 1) {
-#pragma unroll
-      for (int v = 0; v < E / VEC; ++v) {
-        const int k = row_column<TEAM, VEC>(v * VEC);
-        const uint4 q = FULL || k < K ? *reinterpret_cast<const uint4 *>(p + k) : make_uint4(0, 0, 0, 0);
-        w[4 * v] = q.x;
-        w[4 * v + 1] = q.y;
-        w[4 * v + 2] = q.z;
-        w[4 * v + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int k = row_column<TEAM, VEC>(i);
-        w[i] = FULL || k < K ? __float_as_uint(to_f32(p[k])) : 0u;
-      }
-    }
-  }
-  __device__ __forceinline__ void values(f32x2 (&x)[E / 2]) const {
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      if constexpr (VEC > 1 && sizeof(T) == 2) x[i] = widen(w[i], T{});
-      else x[i] = pair_bits(w[2 * i], w[2 * i + 1]);
-    }
-  }
-};
-
 template <typename T, int TEAM, int VEC, int E, bool FULL>
 __device__ __forceinline__ void store_row(T *p, int K, const f32x2 (&y)[E / 2]) {
   if constexpr (VEC == 1) {
@@ -189,20 +155,87 @@ __device__ __forceinline__ void load_params(const void *base, int dtype, size_t 
   }
 }
 
-// Rows fetched ahead of the present one: row m is in slot m mod DEPTH (counted from the block's first row).
+// The copies of one row (of x, or of x and dy) make a group; groups complete in order.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// The block's rows on their way: DEPTH of them in flight in a ring in shared memory, each thread's vectors
+// in slots of its own (asynchronous copies: neither registers nor barriers). 32 to 48 KiB in flight on an
+// SM is what the memory's latency wants; registers for two rows ahead gave less than that. Rows without
+// vectors (VEC = 1) are fetched one ahead, into registers.
 template <typename T, int TEAM, int VEC, int E, bool FULL, int DEPTH>
 struct RowsAhead {
-  RawRow<T, TEAM, VEC, E, FULL> row[DEPTH];
+  static constexpr int NV = E / VEC;
+  uint32_t slot;  // shared address of this thread's first vector
+  int threads;
 
-  __device__ __forceinline__ void start(const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
+  // Bytes of shared memory a block needs.
+  static constexpr int bytes(int threads) { return threads * DEPTH * E * static_cast<int>(sizeof(T)); }
+
+  __device__ __forceinline__ void fetch(int d, const T *p, int K, bool there) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (m0 + d < m1) row[d].load(x0 + (m0 + d) * stride, K);
+    for (int v = 0; v < NV; ++v) {
+      const int k = row_column<TEAM, VEC>(v * VEC);
+      if (there && (FULL || k < K))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + ((d * NV + v) * threads) * 16), "l"(p + k) : "memory");
+    }
   }
-  // row m's values; fetches row m + DEPTH into its slot
-  __device__ __forceinline__ void take(int slot, const T *x0, size_t stride, int64_t m, int64_t m1, int K, f32x2 (&x)[E / 2]) {
-    row[slot].values(x);
-    if (m + DEPTH < m1) row[slot].load(x0 + (m + DEPTH) * stride, K);
+  // Row m0 + d into slot d (the block's first rows).
+  __device__ __forceinline__ void start(uint8_t *ring, int d, const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
+    threads = TEAM == 32 ? 32 : blockDim.x;
+    slot = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
+    fetch(d, x0 + (m0 + d) * stride, K, m0 + d < m1);
+  }
+  // The values of the row in slot d.
+  __device__ __forceinline__ void take(int d, int K, f32x2 (&x)[E / 2]) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (FULL || row_column<TEAM, VEC>(v * VEC) < K)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(slot + ((d * NV + v) * threads) * 16)
+                     : "memory");
+      f32x2 *to = x + v * VEC / 2;
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = widen(w[i], T{});
+      } else {
+        to[0] = pair_bits(w[0], w[1]);
+        to[1] = pair_bits(w[2], w[3]);
+      }
+    }
+  }
+  // Row m + DEPTH into row m's slot d, once its values have been used.
+  __device__ __forceinline__ void refill(int d, const T *x0, size_t stride, int64_t m, int64_t m1, int K) {
+    fetch(d, x0 + (m + DEPTH) * stride, K, m + DEPTH < m1);
+  }
+};
+
+template <typename T, int TEAM, int E, bool FULL, int DEPTH>
+struct RowsAhead<T, TEAM, 1, E, FULL, DEPTH> {
+  float next[E];
+
+  static constexpr int bytes(int) { return 0; }
+  __device__ __forceinline__ void fetch(const T *p, int K) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int k = row_column<TEAM, 1>(i);
+      next[i] = FULL || k < K ? to_f32(p[k]) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void start(uint8_t *, int d, const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
+    if (d == 0 && m0 < m1) fetch(x0 + m0 * stride, K);
+  }
+  __device__ __forceinline__ void take(int, int, f32x2 (&x)[E / 2]) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = pair(next[2 * i], next[2 * i + 1]);
+  }
+  __device__ __forceinline__ void refill(int, const T *x0, size_t stride, int64_t m, int64_t m1, int K) {
+    if (m + 1 < m1) fetch(x0 + (m + 1) * stride, K);
   }
 };
 
