@@ -6,6 +6,9 @@ Each .cu file under csrc/ is compiled to an object in _build/ (rebuilt when it o
 changed) and linked with the static CUDA runtime into bit_rank_compensated_b200/libsvdq.so.
 The eigen-solver library used by the offline prepare step is loaded at run time; the path of
 the copy bundled with the installed nvidia-cusolver wheel is baked in as a hint.
+
+csrc/binding.cpp (the Python calls of the operators around the projections) is compiled against the
+installed torch into bit_rank_compensated_b200/_binding.so.
 """
 from __future__ import annotations
 
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsvdq.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -51,6 +55,31 @@ def _newest_header() -> float:
     return max(os.path.getmtime(h) for h in hs)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compiles csrc/binding.cpp against the installed torch."""
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "svdq.h")), os.path.getmtime(__file__))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+
+    import torch
+
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(base, "lib")
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes[1:]],
+           f"-I{INCLUDE}", src, "-o", BINDING, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -72,6 +101,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_binding(force, verbose)
     return LIB
 
 

@@ -509,101 +509,35 @@ def unfused_forward(X, layer, bufs, Y, stream=None):
 
 
 # ---------------------------------------------------------------- operators around the projections
-# Unlike the calls above these check what they are given (shapes, types, devices; ValueError), since
-# their rows may be strided views, and run on the tensors' device whichever is current. A call costs a
-# few microseconds of the host's time, which is what small ones take: messages are only made on failure.
+# These check what they are given (shapes, types, strides, devices; ValueError), since their rows may be
+# strided views, and run on the tensors' device whichever is current. csrc/binding.cpp does that and calls
+# the library: a small call's time is its caller's.
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3, torch.int64: 4}
-_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
-_INT8 = (torch.int8,)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_BOUND = ("layer_norm", "layer_norm_workspace_bytes", "layer_norm_backward", "i8_quantize_rows",
+          "i8_layer_norm_quantize", "i8_workspace_bytes", "i8_gemm", "i8_linear_forward", "rope_axes_table",
+          "rope_axes_apply")
+_binding = None
 
 
-def _run(name: str, t: torch.Tensor, *args):
-    """Calls an entry point on t's device and that device's current stream."""
-    index = t.get_device()
-    fn = getattr(_lib or load(), name)
-    if index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index))
-    if status != SVDQ_OK:
-        _check(name, status)
+def _native():
+    """The compiled calls (csrc/binding.cpp), bound to the loaded library."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing or does not fit the installed torch; build it with "
+                               "`python -m bit_rank_compensated_b200.build`") from e
+        module.bind(*(ctypes.cast(getattr(lib, "svdq_" + name), ctypes.c_void_p).value for name in _BOUND))
+        _binding = module
+    return _binding
 
 
-def _on_stream(stream, fn, *args, **kw):
+def _on_stream(stream, fn, *args):
     """Runs fn with `stream` as the current one, so that what it allocates belongs to that stream."""
     with torch.cuda.stream(stream):
-        return fn(*args, **kw)
-
-
-def _rows(t, name: str, dtypes=_FLOATS):
-    """(rows, columns, row stride) of a matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be a two-dimensional CUDA tensor of {', '.join(map(str, dtypes))}")
-    M, K = t.shape
-    stride, one = t.stride()
-    if M <= 1:
-        stride = K
-    if (one != 1 and K > 1) or stride < K:
-        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
-    return M, K, stride
-
-
-def _vector(t, name: str, n: int, device, dtype=torch.float32):
-    """Address of n contiguous values (of a vector or matrix), or None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous {dtype} values on {device}")
-    return t.data_ptr()
-
-
-def _like(out, X, M: int, K: int, name: str):
-    """A caller's output of X's type, checked, or a new one; and its row stride."""
-    if out is None:
-        return (torch.empty_like(X) if X.is_contiguous() else X.new_empty((M, K))), K
-    m, k, stride = _rows(out, name, (X.dtype,))
-    if (m, k) != (M, K) or out.device != X.device:
-        raise ValueError(f"{name} must be {M} x {K} on {X.device}")
-    return out, stride
-
-
-def _workspace(t, size: int, device):
-    """(address, bytes) of a caller's workspace, or of a new one of `size` bytes, and what keeps it alive."""
-    if t is None:
-        if not size:
-            return None, 0, None
-        t = torch.empty(size, dtype=torch.uint8, device=device)
-    elif t.device != device or not t.is_contiguous():
-        raise ValueError(f"the workspace must be contiguous and on {device}")
-    return t.data_ptr(), t.numel() * t.element_size(), t
-
-
-def _norm_affine(X, M: int, K: int, weight, bias, rows_per_group: int, weight_offset: float, groups: int | None = None):
-    """The C struct of a layer norm's weight and bias ([K] or [groups, K])."""
-    w = b = None
-    w_stride = b_stride = 0
-    n, dtype = groups, torch.float32
-    for i, t in enumerate((weight, bias)):
-        if t is None:
-            continue
-        name = "bias" if i else "weight"
-        g, k, stride = _rows(t if t.dim() == 2 else t[None], name)
-        if k != K or t.device != X.device or (n is not None and g != n) or (w is not None and t.dtype != dtype):
-            raise ValueError(f"weight and bias must be of one type and shape, with {K} columns, on {X.device}")
-        n, dtype = g, t.dtype
-        if i:
-            b, b_stride = t.data_ptr(), stride
-        else:
-            w, w_stride = t.data_ptr(), stride
-    if n is None:
-        n = 1
-    rows = rows_per_group or max(1, -(-M // max(n, 1)))
-    if n < 1 or rows < 1 or n * rows < M:
-        raise ValueError(f"{n} groups of {rows} rows do not cover {M} rows")
-    return NormAffineStruct(w, b, w_stride, b_stride, DTYPES[dtype], n, rows, weight_offset)
+        return fn(*args)
 
 
 def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset: float = 0.0, eps: float = 1e-6,
@@ -615,15 +549,10 @@ def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset
     output will do. Y may be X. With stats also returns mean and rstd (fp32 [M]) for the backward pass."""
     if stream is not None:
         return _on_stream(stream, layer_norm, X, weight, bias, rows_per_group, weight_offset, eps, Y, stats)
-    M, K, x_stride = _rows(X, "X")
-    affine = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
-    Y, y_stride = _like(Y, X, M, K, "Y")
-    mean = rstd = None
-    if stats:
-        mean, rstd = X.new_empty((2, M), dtype=torch.float32).unbind(0)
-    _run("svdq_layer_norm", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K, ctypes.addressof(affine), eps,
-         Y.data_ptr(), y_stride, mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None)
-    return (Y, mean, rstd) if stats else Y
+    r = (_binding or _native()).layer_norm(X, weight, bias, rows_per_group, weight_offset, eps, Y, stats)
+    if r.__class__ is int:
+        _check("svdq_layer_norm", r)
+    return r
 
 
 def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0, weight_offset: float = 0.0, dX=None,
@@ -635,44 +564,11 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0,
     if stream is not None:
         return _on_stream(stream, layer_norm_backward, dY, X, mean, rstd, weight, rows_per_group, weight_offset, dX,
                           groups, need_dX, need_dweight, need_dbias, workspace)
-    M, K, x_stride = _rows(X, "X")
-    m, k, dy_stride = _rows(dY, "dY", (X.dtype,))
-    device = X.device
-    if m != M or k != K or dY.device != device:
-        raise ValueError(f"dY must be {M} x {K} on {device}")
-    affine = _norm_affine(X, M, K, weight, None, rows_per_group, weight_offset, groups)
-    dx_stride, dx, dw, db, sums = K, None, None, None, None
-    if need_dX:
-        dX, dx_stride = _like(dX, X, M, K, "dX")
-        dx = dX.data_ptr()
-    else:
-        dX = None
-    n = affine.groups
-    if need_dweight or need_dbias:
-        sums = X.new_empty((need_dweight + need_dbias, n, K), dtype=torch.float32)
-        dw = sums[0] if need_dweight else None
-        db = sums[-1] if need_dbias else None
-    size = load().svdq_layer_norm_workspace_bytes(M, K, n, affine.rows_per_group) if sums is not None else 0
-    space, size, kept = _workspace(workspace, size, device)
-    _run("svdq_layer_norm_backward", X, dY.data_ptr(), dy_stride, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
-         ctypes.addressof(affine), _vector(mean, "mean", M, device), _vector(rstd, "rstd", M, device), dx, dx_stride,
-         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), space, size)
-    return dX, dw, db
-
-
-def _i8_rows(X, M: int, K: int, xq, x_scale):
-    """Int8 rows and scales: the caller's, checked, or new ones; and their addresses."""
-    if xq is None:
-        xq = X.new_empty((M, K), dtype=torch.int8)
-        q = xq.data_ptr()
-    else:
-        q = _vector(xq, "xq", M * K, X.device, torch.int8)
-    if x_scale is None:
-        x_scale = X.new_empty(M, dtype=torch.float32)
-        s = x_scale.data_ptr()
-    else:
-        s = _vector(x_scale, "x_scale", M, X.device)
-    return xq, x_scale, q, s
+    r = (_binding or _native()).layer_norm_backward(dY, X, mean, rstd, weight, rows_per_group, weight_offset, dX, groups,
+                                                    need_dX, need_dweight, need_dbias, workspace)
+    if r.__class__ is int:
+        _check("svdq_layer_norm_backward", r)
+    return r
 
 
 def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
@@ -680,11 +576,10 @@ def i8_quantize_rows(X, col_scale=None, xq=None, x_scale=None, stream=None):
     weights by output channel."""
     if stream is not None:
         return _on_stream(stream, i8_quantize_rows, X, col_scale, xq, x_scale)
-    M, K, x_stride = _rows(X, "X")
-    xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
-    _run("svdq_i8_quantize_rows", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
-         _vector(col_scale, "col_scale", K, X.device), q, s)
-    return xq, x_scale
+    r = (_binding or _native()).i8_quantize_rows(X, col_scale, xq, x_scale)
+    if r.__class__ is int:
+        _check("svdq_i8_quantize_rows", r)
+    return r
 
 
 def i8_layer_norm_quantize(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset: float = 0.0,
@@ -693,44 +588,27 @@ def i8_layer_norm_quantize(X, weight=None, bias=None, rows_per_group: int = 0, w
     if stream is not None:
         return _on_stream(stream, i8_layer_norm_quantize, X, weight, bias, rows_per_group, weight_offset, eps, xq,
                           x_scale)
-    M, K, x_stride = _rows(X, "X")
-    affine = _norm_affine(X, M, K, weight, bias, rows_per_group, weight_offset)
-    xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
-    _run("svdq_i8_layer_norm_quantize", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M, K,
-         ctypes.addressof(affine), eps, q, s)
-    return xq, x_scale
+    r = (_binding or _native()).i8_layer_norm_quantize(X, weight, bias, rows_per_group, weight_offset, eps, xq, x_scale)
+    if r.__class__ is int:
+        _check("svdq_i8_layer_norm_quantize", r)
+    return r
 
 
 def i8_workspace_bytes(M: int, N: int, K: int) -> int:
     return load().svdq_i8_workspace_bytes(M, N, K)
 
 
-def _i8_weight(wq, w_scale, bias, K: int, device):
-    if not isinstance(wq, torch.Tensor) or wq.dim() != 2 or wq.shape[1] != K:
-        raise ValueError(f"wq must be a matrix of {K} columns")
-    N = wq.shape[0]
-    return (N, _vector(wq, "wq", N * K, device, torch.int8), _vector(w_scale, "w_scale", N, device),
-            None if bias is None else _vector(bias, "bias", N, device))
-
-
 def i8_gemm(xq, x_scale, wq, w_scale, bias=None, Y=None, dtype=torch.bfloat16, workspace=None, stream=None):
     """Y [M, N] = (xq wq^T) * x_scale[:, None] * w_scale + bias from int8 rows, with exact integer sums."""
     if stream is not None:
         return _on_stream(stream, i8_gemm, xq, x_scale, wq, w_scale, bias, Y, dtype, workspace)
-    M, K, _ = _rows(xq, "xq", _INT8)
-    device = xq.device
-    if dtype not in _FLOATS:
-        raise ValueError(f"dtype must be one of {_FLOATS}")
-    N, w, ws, b = _i8_weight(wq, w_scale, bias, K, device)
-    x, xs = _vector(xq, "xq", M * K, device, torch.int8), _vector(x_scale, "x_scale", M, device)
-    if Y is None:
-        Y = xq.new_empty((M, N), dtype=dtype)
-        y = Y.data_ptr()
-    else:
-        y = _vector(Y, "Y", M * N, device, dtype)
-    space, size, kept = _workspace(workspace, load().svdq_i8_workspace_bytes(M, N, K), device)
-    _run("svdq_i8_gemm", xq, x, xs, M, w, ws, b, N, K, y, DTYPES[dtype], space, size)
-    return Y
+    code = DTYPES.get(dtype, 9)
+    if code > 2:
+        raise ValueError("dtype must be bf16, fp16 or fp32")
+    r = (_binding or _native()).i8_gemm(xq, x_scale, wq, w_scale, bias, Y, code, workspace)
+    if r.__class__ is int:
+        _check("svdq_i8_gemm", r)
+    return r
 
 
 def i8_linear_forward(X, wq, w_scale, bias=None, col_scale=None, xq=None, x_scale=None, Y=None, workspace=None,
@@ -740,34 +618,13 @@ def i8_linear_forward(X, wq, w_scale, bias=None, col_scale=None, xq=None, x_scal
     i8_workspace_bytes says."""
     if stream is not None:
         return _on_stream(stream, i8_linear_forward, X, wq, w_scale, bias, col_scale, xq, x_scale, Y, workspace)
-    M, K, x_stride = _rows(X, "X")
-    device = X.device
-    N, w, ws, b = _i8_weight(wq, w_scale, bias, K, device)
-    size = load().svdq_i8_workspace_bytes(M, N, K)
-    if xq is None and x_scale is None and workspace is None:
-        # one allocation: the rows (a multiple of 16 bytes), the workspace, the scales
-        rows = M * K
-        kept = X.new_empty(rows + size + 4 * M, dtype=torch.int8)
-        q = kept.data_ptr()
-        space = q + rows if size else None
-        s = q + rows + size
-    else:
-        xq, x_scale, q, s = _i8_rows(X, M, K, xq, x_scale)
-        space, size, kept = _workspace(workspace, size, device)
-    if Y is None:
-        Y = X.new_empty((M, N))
-        y = Y.data_ptr()
-    else:
-        y = _vector(Y, "Y", M * N, device, X.dtype)
-    _run("svdq_i8_linear_forward", X, X.data_ptr(), x_stride, DTYPES[X.dtype], M,
-         None if col_scale is None else _vector(col_scale, "col_scale", K, device), w, ws, b, N, K, q, s, y, space, size)
-    return Y
+    r = (_binding or _native()).i8_linear_forward(X, wq, w_scale, bias, col_scale, xq, x_scale, Y, workspace)
+    if r.__class__ is int:
+        _check("svdq_i8_linear_forward", r)
+    return r
 
 
-# svdq_rope_axes, svdq_positions and svdq_heads as bytes in the C layout (quicker to make than ctypes structs)
-_ROPE_AXES = struct.Struct("@7if")
-_POSITIONS = struct.Struct("@PiNN")
-_HEADS = struct.Struct("@PiNN")
+_ROPE_AXES = struct.Struct("@7if")  # svdq_rope_axes
 
 
 class RopeAxes:
@@ -778,56 +635,22 @@ class RopeAxes:
     Pair p is columns (2p, 2p + 1), or with halves (p, p + sum(pairs))."""
 
     def __init__(self, pairs, theta: float = 10000.0, shared_ladder: bool = False, halves: bool = False):
-        if not 1 <= len(pairs) <= 4 or min(pairs) < 1:
-            raise ValueError("one to four axes of at least one pair are supported")
-        self.pairs, self.theta = tuple(pairs), float(theta)
-        self.n_pairs = sum(pairs)
-        self.s = _ROPE_AXES.pack(len(pairs), *self.pairs, *(0,) * (4 - len(pairs)), bool(shared_ladder), bool(halves), theta)
-
-
-def _positions(pos, axes: RopeAxes, M=None, device=None):
-    if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype not in (torch.int64, torch.int32, torch.float32):
-        raise ValueError("pos must be a CUDA tensor of int32, int64 or fp32")
-    if pos.dim() == 1:
-        pos = pos[:, None]
-    if (pos.dim() != 2 or pos.shape[1] != len(axes.pairs) or (M is not None and pos.shape[0] != M)
-            or (device is not None and pos.device != device)):
-        raise ValueError(f"pos must be [tokens, {len(axes.pairs)}], with the heads' tokens and device")
-    token, axis = pos.stride()
-    return _POSITIONS.pack(pos.data_ptr(), DTYPES[pos.dtype], token, axis)
+        n = len(pairs)
+        if not 1 <= n <= 4 or not 1 <= min(pairs) <= max(pairs) <= 256:
+            raise ValueError("one to four axes of 1 to 256 pairs are supported")
+        self.pairs, self.theta, self.n_pairs = tuple(pairs), theta, sum(pairs)
+        self.s = _ROPE_AXES.pack(n, *pairs, *(0,) * (4 - n), bool(shared_ladder), bool(halves), theta)
 
 
 def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
-    """(cos, sin) of every token and pair, fp32 [M, pairs, 2], from position ids [M, axes]: with 64 pairs the
-    table that gemm_w4a4_lora_up_qk_norm_rope and qk_norm_rope take."""
+    """(cos, sin) of every token and pair, fp32 [M, pairs, 2], from position ids [M, axes] (int32, int64 or fp32):
+    with 64 pairs the table that gemm_w4a4_lora_up_qk_norm_rope and qk_norm_rope take."""
     if stream is not None:
         return _on_stream(stream, rope_axes_table, pos, axes, table)
-    p = _positions(pos, axes)
-    M, n = pos.shape[0], axes.n_pairs
-    if table is None:
-        table = pos.new_empty((M, n, 2), dtype=torch.float32)
-        to = table.data_ptr()
-    else:
-        to = _vector(table, "table", 2 * M * n, pos.device)
-    _run("svdq_rope_axes_table", pos, p, M, axes.s, to)
-    return table
-
-
-def _heads(t, out, name: str, M: int, D: int, dtype, device):
-    """svdq_heads of heads [M, H, D] and of their output, and the output (a new one unless given)."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[0] != M or t.shape[2] != D:
-        raise ValueError(f"{name} must be [{M}, heads, {D}] of {dtype} on {device}")
-    token, head, one = t.stride()
-    H = t.shape[1]
-    source = _HEADS.pack(t.data_ptr(), H, token, head)
-    if out is None:
-        out = torch.empty_like(t)
-    elif out.shape != t.shape or out.dtype != dtype or out.device != device:
-        raise ValueError(f"{name}_out must be like {name}")
-    token, head, last = out.stride()
-    if one != 1 or last != 1:
-        raise ValueError(f"the columns of {name} and its output must be contiguous")
-    return source, _HEADS.pack(out.data_ptr(), H, token, head), out
+    r = (_binding or _native()).rope_axes_table(pos, axes.s, table)
+    if r.__class__ is int:
+        _check("svdq_rope_axes_table", r)
+    return r
 
 
 def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -836,18 +659,10 @@ def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None
     be q and k. Returns (q_out, k_out)."""
     if stream is not None:
         return _on_stream(stream, rope_axes_apply, q, k, pos, axes, inverse, q_out, k_out)
-    dtype, device = q.dtype, q.device
-    if q.dim() != 3 or not q.is_cuda or dtype not in _FLOATS:
-        raise ValueError("q must be a CUDA tensor [tokens, heads, columns] of a floating type of 16 or 32 bits")
-    M, _, D = q.shape
-    qi, qo, q_out = _heads(q, q_out, "q", M, D, dtype, device)
-    if k is None:
-        ki = ko = k_out = None
-    else:
-        ki, ko, k_out = _heads(k, k_out, "k", M, D, dtype, device)
-    p = _positions(pos, axes, M, device)
-    _run("svdq_rope_axes_apply", q, qi, qo, ki, ko, DTYPES[dtype], M, D, p, axes.s, bool(inverse))
-    return q_out, k_out
+    r = (_binding or _native()).rope_axes_apply(q, k, pos, axes.s, inverse, q_out, k_out)
+    if r.__class__ is int:
+        _check("svdq_rope_axes_apply", r)
+    return r
 
 
 def selftest_wait_timeout(limit_us: int, stream=None) -> None:
