@@ -102,6 +102,16 @@ svdq_status check_gemm(const int8_t *xq, const float *x_scale, int M, const int8
   return SVDQ_OK;
 }
 
+svdq_status check_quantize(const void *X, size_t x_stride, int dtype, int M, int K, const float *col_scale,
+                           const int8_t *xq, const float *x_scale) {
+  if (!is_float(dtype) || M < 0 || M > kMaxRows || K < 16 || K % 16 || K > kMaxI8Columns || x_stride < static_cast<size_t>(K))
+    return SVDQ_ERR_INVALID_ARG;
+  if (M > 0 && (!X || !xq || !x_scale)) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned(X, elem_bytes(dtype)) || !aligned(col_scale, 4) || !aligned16(xq) || !aligned(x_scale, 4))
+    return SVDQ_ERR_MISALIGNED;
+  return SVDQ_OK;
+}
+
 svdq_status check_heads(const svdq_heads *in, const svdq_heads *out, int M, int head_dim, size_t e) {
   if (!in || !out || in->heads < 1 || in->heads > kMaxHeads || out->heads != in->heads) return SVDQ_ERR_INVALID_ARG;
   const size_t d = static_cast<size_t>(head_dim);
@@ -181,14 +191,10 @@ svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, const voi
 
 svdq_status svdq_i8_quantize_rows(const void *X, size_t x_stride, int dtype, int M, int K, const float *col_scale,
                                   int8_t *xq, float *x_scale, void *stream) {
-  if (!is_float(dtype) || M < 0 || M > kMaxRows || K < 16 || K % 16 || K > kMaxI8Columns || x_stride < static_cast<size_t>(K))
-    return SVDQ_ERR_INVALID_ARG;
-  if (M > 0 && (!X || !xq || !x_scale)) return SVDQ_ERR_INVALID_ARG;
-  if (!aligned(X, elem_bytes(dtype)) || !aligned(col_scale, 4) || !aligned16(xq) || !aligned(x_scale, 4))
-    return SVDQ_ERR_MISALIGNED;
+  svdq_status st = check_quantize(X, x_stride, dtype, M, K, col_scale, xq, x_scale);
+  if (st != SVDQ_OK) return st;
   DeviceState *d = nullptr;
-  svdq_status st = device_check(&d);
-  if (st != SVDQ_OK || M == 0) return st;
+  if ((st = device_check(&d)) != SVDQ_OK || M == 0) return st;
   const QuantRowsLaunch a{X, x_stride, dtype, M, K, col_scale, xq, x_scale, d->num_sms, static_cast<cudaStream_t>(stream)};
   return done(launch_i8_quantize_rows(a));
 }
@@ -232,6 +238,16 @@ svdq_status svdq_i8_linear_forward(const void *X, size_t x_stride, int dtype, in
                                    float *x_scale, void *Y, void *workspace, size_t workspace_bytes, void *stream) {
   svdq_status st = check_gemm(xq, x_scale, M, wq, w_scale, bias, N, K, Y, dtype, workspace, workspace_bytes);
   if (st != SVDQ_OK) return st;
+  if (M > 0 && i8_few_fits(M, K)) {
+    // few tokens: quantized where they are multiplied, in one launch
+    if ((st = check_quantize(X, x_stride, dtype, M, K, col_scale, xq, x_scale)) != SVDQ_OK) return st;
+    DeviceState *d = nullptr;
+    if ((st = device_check(&d)) != SVDQ_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const QuantRowsLaunch q{X, x_stride, dtype, M, K, col_scale, xq, x_scale, d->num_sms, s};
+    const I8GemmLaunch g{xq, wq, x_scale, w_scale, bias, M, N, K, Y, dtype, workspace, d, s};
+    if (i8_few_quantizes(q)) return done(launch_i8_few_quantized(q, g));
+  }
   st = svdq_i8_quantize_rows(X, x_stride, dtype, M, K, col_scale, xq, x_scale, stream);
   if (st != SVDQ_OK) return st;
   return svdq_i8_gemm(xq, x_scale, M, wq, w_scale, bias, N, K, Y, dtype, workspace, workspace_bytes, stream);

@@ -313,6 +313,7 @@ cudaError_t launch_t(const I8GemmLaunch &g) {
 size_t i8_gemm_workspace_bytes(int, int, int) { return 0; }
 
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g) {
+  if (i8_few_fits(g.M, g.K)) return launch_i8_few(g);
   if (static_cast<int64_t>((g.M + 2 * BM - 1) / (2 * BM)) * ((g.N + 63) / 64) >= (1ll << 31)) return cudaErrorInvalidValue;
   if (g.y_dtype == SVDQ_F32) return launch_t<float>(g);
   if (g.y_dtype == SVDQ_F16) return launch_t<__half>(g);

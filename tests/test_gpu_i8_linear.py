@@ -121,7 +121,10 @@ def test_sums_are_exact_integers(M):
 
 
 @pytest.mark.parametrize("M,N,K,dtype,smooth", [(1, 512, 1024, BF16, True), (6, 272, 528, F16, False),
-                                                (140, 1040, 2064, F32, True), (600, 512, 1536, BF16, False)])
+                                                (140, 1040, 2064, F32, True), (600, 512, 1536, BF16, False),
+                                                (1, 48, 16, F32, False), (2, 96, 496, F16, True), (3, 528, 2560, F32, True),
+                                                (4, 1040, 4112, BF16, False), (5, 4096, 9216, F16, True),
+                                                (8, 272, 12288, BF16, True), (8, 64, 1040, F32, False), (1, 32, 65536, BF16, True)])
 def test_linear_forward(M, N, K, dtype, smooth):
     """From floating rows to floating rows; the weight quantized by the same rows' quantizer under the inverse smoothing."""
     svdq = _svdq()
@@ -143,6 +146,32 @@ def test_linear_forward(M, N, K, dtype, smooth):
     hx, hw = s.double()[:, None] / 2, ws.double()[None] / 2
     assert bool(((y - full).abs() <= (hx * wa.sum(1) + xa.sum(1, keepdim=True) * hw + K * hx * hw) * (1 + 1e-4)
                  + 8 * R.U * (xa @ wa.t())).all())
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 9, 40])
+@pytest.mark.parametrize("dtype", R.FLOATS)
+def test_few_tokens_and_many_give_the_same_bits(M, dtype):
+    """The quantizer and the product are exact, so a token's output does not depend on how many come with it, nor on
+    whether its rows are given as int8 or as (strided, unaligned) floating ones."""
+    svdq = _svdq()
+    X = _acts(40, 1100, dtype, 60)[:, 3:3 + 1040]
+    wq, ws = _codes(272, 1040, 61), torch.rand(272, generator=_gen(62), device="cuda") * 1e-3
+    col = torch.rand(1040, generator=_gen(63), device="cuda") + 0.5
+    every = svdq.i8_gemm(*svdq.i8_quantize_rows(X, col), wq, ws, dtype=dtype)
+    assert torch.equal(svdq.i8_linear_forward(X[:M], wq, ws, col_scale=col), every[:M])
+    assert torch.equal(svdq.i8_linear_forward(X[:M].contiguous(), wq, ws, col_scale=col), every[:M])
+    assert torch.equal(svdq.i8_gemm(*svdq.i8_quantize_rows(X[:M], col), wq, ws, dtype=dtype), every[:M])
+
+
+def test_few_tokens_special_rows():
+    """Zeros, infinities and NaNs among few tokens: as among many."""
+    svdq = _svdq()
+    X = _acts(4, 512, BF16, 65)
+    X[0], X[2, 7], X[3, 500] = 0, float("inf"), float("nan")
+    wq, ws = _codes(48, 512, 66), torch.ones(48, device="cuda")
+    b = torch.arange(48, device="cuda").float()
+    Y = svdq.i8_linear_forward(X, wq, ws, b)
+    assert torch.equal(Y[0].float(), b) and bool(Y[1].isfinite().all()) and bool(Y[2:].isnan().all())
 
 
 def test_no_rows_and_caller_buffers():
