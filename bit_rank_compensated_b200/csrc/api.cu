@@ -132,6 +132,18 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t middle, uint64_t outer,
+                 uint64_t elem_bytes, uint32_t box_inner, uint32_t box_middle, CUtensorMapSwizzle swz) {
+  std::call_once(g_encode_once, init_encode);
+  if (!g_encode) return false;
+  const cuuint64_t dims[3] = {inner, middle, outer};
+  const cuuint64_t strides[2] = {inner * elem_bytes, inner * middle * elem_bytes};
+  const cuuint32_t box[3] = {box_inner, box_middle, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 CUtensorMapSwizzle swizzle_for_row_bytes(uint32_t b) {

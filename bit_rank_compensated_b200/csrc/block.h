@@ -92,11 +92,26 @@ struct RopeLaunch {
 cudaError_t launch_rope_table(const RopeLaunch &a);
 cudaError_t launch_rope_apply(const RopeLaunch &a);
 
-// Lets a kernel have `bytes` of dynamic shared memory on the current device.
+// Lets a kernel have `bytes` of dynamic shared memory on the current device. The attribute costs the host
+// some 3 us, so what a thread has set is remembered (a slot per kernel and device, lost to another one at
+// worst: setting it again is harmless).
 template <typename... Args>
 cudaError_t allow_smem(void (*kern)(Args...), int bytes) {
   if (bytes <= 40 * 1024) return cudaSuccess;  // within the default, static arrays included
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  struct Granted {
+    const void *kern;
+    int device, bytes;
+  };
+  static thread_local Granted slots[64];
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const void *key = reinterpret_cast<const void *>(kern);
+  Granted &s = slots[(reinterpret_cast<uintptr_t>(key) / 64 + static_cast<uintptr_t>(device) * 17) % 64];
+  if (s.kern == key && s.device == device && s.bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) s = {key, device, bytes};
+  return e;
 }
 
 // Launches a kernel that waits (grid_dep_wait) before it touches global memory, so that its start may

@@ -23,6 +23,10 @@ svdq_status device_check(DeviceState **out);
 bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
 
+// 3-d tensor map of a contiguous array; boxes of one outer index.
+bool make_map_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t middle, uint64_t outer,
+                 uint64_t elem_bytes, uint32_t box_inner, uint32_t box_middle, CUtensorMapSwizzle swz);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace svdq
