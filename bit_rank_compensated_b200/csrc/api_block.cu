@@ -148,7 +148,7 @@ svdq_status svdq_layer_norm(const void *X, size_t x_stride, int dtype, int M, in
 
 size_t svdq_layer_norm_workspace_bytes(int M, int K, int groups, int rows_per_group) {
   if (M < 1 || K < 1 || K > kMaxNormColumns || groups < 1 || rows_per_group < 1) return 0;
-  return layer_norm_partial_bytes(M, K, groups, rows_per_group);
+  return layer_norm_partial_bytes(M, K, rows_per_group);
 }
 
 svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, const void *X, size_t x_stride, int dtype, int M,

@@ -41,7 +41,7 @@ struct NormLaunch {
 cudaError_t launch_layer_norm(const NormLaunch &a);
 cudaError_t launch_layer_norm_quantize(const NormLaunch &a);
 cudaError_t launch_layer_norm_backward(const NormLaunch &a);
-size_t layer_norm_partial_bytes(int M, int K, int groups, int rows_per_group);
+size_t layer_norm_partial_bytes(int M, int K, int rows_per_group);
 
 // int8 rows of X (or of X * col_scale).
 struct QuantRowsLaunch {

@@ -87,7 +87,7 @@ __device__ __forceinline__ void quantize(const FewArgs &a, int8_t *codes, float 
 #pragma unroll
   for (int i = 0; i < WPR; ++i) t = max(t, top[m * WPR + i]);
   const RowScale r = row_scale(t);
-  if (part == 0 && lane == 0) scale[m] = r.scale;
+  if (part == 0 && lane == 0) scale[m] = scale_of(r);
   int8_t *q = codes + static_cast<size_t>(m) * a.K;
 #pragma unroll 2
   for (int k = (part * 32 + lane) * V; k < a.K; k += WPR * 32 * V) {

@@ -9,7 +9,7 @@
 namespace svdq {
 
 struct RowScale {
-  float scale;  // max / 127; NaN for a row with an infinity or a NaN
+  float max;    // the row's largest |v|; NaN for a row with an infinity or a NaN
   float c;      // about 127 / max; NaN where that is no fit for fp32 (every code then takes the exact way)
   float by;     // power of two that brings the row's values where the exact way's arithmetic is exact
   float top;    // by * max
@@ -23,9 +23,12 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
   const float max = __uint_as_float(top_bits);
   const float by = max < 0x1p-60f ? 0x1p90f : (max > 0x1p100f ? 0x1p-30f : 1.0f);
   const float top = max * by;
-  const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
-  return {__fdiv_rn(max, 127.0f), by == 1.0f ? inv : nan, by, top, inv};
+  const float inv = top > 0.0f ? __fdividef(127.0f, top) : 0.0f;  // within 2 units in the last place
+  return {max, by == 1.0f ? inv : nan, by, top, inv};
 }
+
+// The scale of a row: correctly rounded, and so worth one thread's time only.
+__device__ __forceinline__ float scale_of(const RowScale &r) { return __fdiv_rn(r.max, 127.0f); }
 
 // rint(127 v / max), ties to even, as the exact quotient rounds: with k below the quotient, 127 |v| is
 // compared with (k + 1/2) top. The former is p + e (a product and its rounding error); near the border
@@ -43,7 +46,7 @@ __device__ __forceinline__ int i8_code(float v, const RowScale &r) {
 }
 
 // Codes of 2 N values, the first in the lowest byte of o[0] (N = 1: both in o[0]). Adding 1.5 * 2^23 rounds
-// v c to an integer whose last byte is the code; v c is within 127 * 2^-23 of the quotient, so that
+// v c to an integer whose last byte is the code; v c is within 127 * 2^-21 of the quotient, so that
 // decides unless v c lies that near to a border (0.4999 of a step from the integer): hardly any value
 // does, and one test serves them all.
 template <int N>

@@ -33,21 +33,21 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
     copies_commit();
   }
   f32x2 c[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) c[i] = both(1.0f);  // exact
   if (a.col_scale) load_params<TEAM, VEC, E, FULL>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
   int slot = 0;
   for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2];
     copies_wait<kDepth<T> - 1>();
     ahead.take(slot, a.K, x);
+    if (a.col_scale) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c[i]);
+      for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c[i]);
+    }
     const RowScale r = row_scale(top(thread_top(x), turn));
     ahead.refill(slot, x0, a.x_stride, m, m1, a.K);
     copies_commit();
     slot = slot + 1 == kDepth<T> ? 0 : slot + 1;
-    if (threadIdx.x == 0) a.x_scale[m] = r.scale;
+    if (threadIdx.x == 0) a.x_scale[m] = scale_of(r);
     store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
   }
 }
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(1024) k_quantize_long_rows(QuantRowsLaunch a) 
   uint32_t t = 0, turn = 0;
   for (int k = threadIdx.x; k < a.K; k += 1024) t = max(t, __float_as_uint(value(k)) & 0x7fffffffu);
   const RowScale r = row_scale(top(t, turn));
-  if (threadIdx.x == 0) a.x_scale[m] = r.scale;
+  if (threadIdx.x == 0) a.x_scale[m] = scale_of(r);
   for (int k = threadIdx.x; k < a.K; k += 1024) a.xq[m * a.K + k] = static_cast<int8_t>(i8_code(value(k), r));
 }
 
