@@ -83,6 +83,7 @@ svdq_status check_axes(const svdq_positions *pos, int M, const svdq_rope_axes *a
   if (!pos->data && M > 0) return SVDQ_ERR_INVALID_ARG;
   a->pos = *pos;
   a->axes = *ax;
+  a->log2_theta = log2(static_cast<double>(ax->theta));
   a->n_pairs = P;
   a->M = M;
   return aligned(pos->data, elem_bytes(pos->dtype)) ? SVDQ_OK : SVDQ_ERR_MISALIGNED;

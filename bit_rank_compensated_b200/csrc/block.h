@@ -80,6 +80,7 @@ size_t i8_gemm_workspace_bytes(int M, int N, int K);
 struct RopeLaunch {
   svdq_positions pos;
   svdq_rope_axes axes;
+  double log2_theta;
   int n_pairs;
   int M;
   float *table;

@@ -86,7 +86,7 @@ __device__ __forceinline__ void quantize(const FewArgs &a, int8_t *codes, float 
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < WPR; ++i) t = max(t, top[m * WPR + i]);
-  const RowScale r = row_scale(t);
+  const RowScale r = row_scale<false>(t);
   if (part == 0 && lane == 0) scale[m] = scale_of(r);
   int8_t *q = codes + static_cast<size_t>(m) * a.K;
 #pragma unroll 2
@@ -95,7 +95,7 @@ __device__ __forceinline__ void quantize(const FewArgs &a, int8_t *codes, float 
     if (m < a.M) {
       f32x2 v[V / 2];
       vector(k, v);
-      i8_pack<V / 2>(v, r, o);
+      i8_pack<V / 2, false>(v, r, o);
     }
     if constexpr (V == 8) *reinterpret_cast<uint2 *>(q + k) = make_uint2(o[0], o[1]);
     else *reinterpret_cast<uint32_t *>(q + k) = o[0];

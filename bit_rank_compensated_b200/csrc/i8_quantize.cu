@@ -34,6 +34,11 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
   }
   f32x2 c[E / 2];
   if (a.col_scale) load_params<TEAM, VEC, E, FULL>(a.col_scale, SVDQ_F32, 0, a.K, 0.0f, c);
+  auto write = [&]<bool SHORT>(int64_t m, const f32x2(&x)[E / 2], uint32_t most) {
+    const RowScale r = row_scale<SHORT>(most);
+    if (threadIdx.x == 0) a.x_scale[m] = scale_of(r);
+    store_codes<TEAM, VEC, E, FULL, SHORT>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
+  };
   int slot = 0;
   for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2];
@@ -43,12 +48,12 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c[i]);
     }
-    const RowScale r = row_scale(top(thread_top(x), turn));
+    const uint32_t most = top(thread_top(x), turn);
     ahead.refill(slot, x0, a.x_stride, m, m1, a.K);
     copies_commit();
     slot = slot + 1 == kDepth<T> ? 0 : slot + 1;
-    if (threadIdx.x == 0) a.x_scale[m] = scale_of(r);
-    store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
+    if (sizeof(T) == 2 && !a.col_scale) write.template operator()<true>(m, x, most);
+    else write.template operator()<false>(m, x, most);
   }
 }
 
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(1024) k_quantize_long_rows(QuantRowsLaunch a) 
   auto value = [&](int k) { return a.col_scale ? __fmul_rn(to_f32(x[k]), a.col_scale[k]) : to_f32(x[k]); };
   uint32_t t = 0, turn = 0;
   for (int k = threadIdx.x; k < a.K; k += 1024) t = max(t, __float_as_uint(value(k)) & 0x7fffffffu);
-  const RowScale r = row_scale(top(t, turn));
+  const RowScale r = row_scale<false>(top(t, turn));
   if (threadIdx.x == 0) a.x_scale[m] = scale_of(r);
   for (int k = threadIdx.x; k < a.K; k += 1024) a.xq[m * a.K + k] = static_cast<int8_t>(i8_code(value(k), r));
 }

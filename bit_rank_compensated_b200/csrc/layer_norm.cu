@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
       store_row<T, TEAM, VEC, E, FULL>(static_cast<T *>(a.Y) + m * a.y_stride, a.K, x);
     } else {
       // columns from K on are zeros still: their x and b are
-      const RowScale r = row_scale(top(thread_top(x), tmax));
+      const RowScale r = row_scale<false>(top(thread_top(x), tmax));
       if (threadIdx.x == 0) a.x_scale[m] = scale_of(r);
-      store_codes<TEAM, VEC, E, FULL>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
+      store_codes<TEAM, VEC, E, FULL, false>(a.xq + static_cast<size_t>(m) * a.K, a.K, x, r);
     }
   }
 }

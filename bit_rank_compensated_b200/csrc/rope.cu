@@ -23,12 +23,12 @@ struct Ladder {
   double turns[kMaxPairs];
   uint8_t axis[kMaxPairs];
 
-  __device__ __forceinline__ void fill(const svdq_rope_axes &ax, int P) {
+  __device__ __forceinline__ void fill(const svdq_rope_axes &ax, int P, double log2_theta) {
     for (int p = threadIdx.x; p < P; p += blockDim.x) {
       int a = 0, i = p;
       while (i >= ax.pairs[a]) i -= ax.pairs[a++];
       const double power = ax.shared_ladder ? static_cast<double>(p) / P : static_cast<double>(i) / ax.pairs[a];
-      turns[p] = exp2(-power * log2(static_cast<double>(ax.theta))) * 0.15915494309189533577;  // / 2 pi
+      turns[p] = exp2(-power * log2_theta) * 0.15915494309189533577;  // / 2 pi
       axis[p] = static_cast<uint8_t>(a);
     }
   }
@@ -48,7 +48,7 @@ struct Ladder {
 // A thread keeps its pair and takes every lanes-th token of the block's share.
 __global__ void __launch_bounds__(kThreads) k_rope_table(RopeLaunch a, int tokens) {
   __shared__ Ladder ladder;
-  ladder.fill(a.axes, a.n_pairs);
+  ladder.fill(a.axes, a.n_pairs, a.log2_theta);
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_apply(RopeLaunch a, int units
   __shared__ Ladder ladder;
   __shared__ float2 cs_s[2][kMaxPairs];
   const int P = a.n_pairs;
-  ladder.fill(a.axes, P);
+  ladder.fill(a.axes, P, a.log2_theta);
   grid_dep_wait();
   grid_dep_launch();
   const int u = threadIdx.x % units, lane = threadIdx.x / units;

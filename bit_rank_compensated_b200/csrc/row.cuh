@@ -64,7 +64,7 @@ __device__ __forceinline__ void store_row(T *p, int K, const f32x2 (&y)[E / 2]) 
 }
 
 // The int8 codes of a row, VEC bytes a store, each vector as soon as it is formed.
-template <int TEAM, int VEC, int E, bool FULL>
+template <int TEAM, int VEC, int E, bool FULL, bool SHORT>
 __device__ __forceinline__ void store_codes(int8_t *p, int K, const f32x2 (&x)[E / 2], const RowScale &r) {
 #pragma unroll
   for (int v = 0; v < E / (VEC > 1 ? VEC : 2); ++v) {
@@ -72,11 +72,11 @@ __device__ __forceinline__ void store_codes(int8_t *p, int K, const f32x2 (&x)[E
     if constexpr (VEC > 1) {
       const int k = row_column<TEAM, VEC>(v * VEC);
       if (!FULL && k >= K) continue;
-      i8_pack<VEC / 2>(x + v * VEC / 2, r, o);
+      i8_pack<VEC / 2, SHORT>(x + v * VEC / 2, r, o);
       if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p + k) = make_uint2(o[0], o[1]);
       else *reinterpret_cast<uint32_t *>(p + k) = o[0];
     } else {
-      i8_pack<1>(x + v, r, o);
+      i8_pack<1, SHORT>(x + v, r, o);
       const int k0 = row_column<TEAM, 1>(2 * v), k1 = row_column<TEAM, 1>(2 * v + 1);
       if (FULL || k0 < K) p[k0] = static_cast<int8_t>(o[0]);
       if (FULL || k1 < K) p[k1] = static_cast<int8_t>(o[0] >> 8);
