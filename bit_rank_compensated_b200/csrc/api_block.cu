@@ -115,12 +115,16 @@ svdq_status check_quantize(const void *X, size_t x_stride, int dtype, int M, int
 
 svdq_status check_heads(const svdq_heads *in, const svdq_heads *out, int M, int head_dim, size_t e) {
   if (!in || !out || in->heads < 1 || in->heads > kMaxHeads || out->heads != in->heads) return SVDQ_ERR_INVALID_ARG;
-  const size_t d = static_cast<size_t>(head_dim);
   for (const svdq_heads *h : {in, out}) {
-    if ((!h->data && M > 0) || (h->heads > 1 && h->head_stride < d) || (M > 1 && h->token_stride < d))
-      return SVDQ_ERR_INVALID_ARG;
+    if (!h->data && M > 0) return SVDQ_ERR_INVALID_ARG;
     if (!aligned(h->data, e)) return SVDQ_ERR_MISALIGNED;
   }
+  // an output's heads must not overlap, in either order of tokens and heads (an input's may: shared heads)
+  const size_t d = static_cast<size_t>(head_dim), t = out->token_stride, h = out->head_stride;
+  const size_t tokens = M > 0 ? static_cast<size_t>(M) : 1, heads = static_cast<size_t>(out->heads);
+  const bool heads_inside = (heads == 1 || h >= d) && (tokens == 1 || t >= (heads - 1) * h + d);
+  const bool tokens_inside = (tokens == 1 || t >= d) && (heads == 1 || h >= (tokens - 1) * t + d);
+  if (!heads_inside && !tokens_inside) return SVDQ_ERR_INVALID_ARG;
   return SVDQ_OK;
 }
 

@@ -373,8 +373,9 @@ SVDQ_API svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, 
  * svdq_i8_gemm: the product.  Y device, M x N of y_dtype, contiguous, 16-byte aligned.
  *     workspace  device, 16-byte aligned, at least svdq_i8_workspace_bytes(M, N, K) bytes (may be 0,
  *                then NULL is fine): partial sums where few tokens leave the K axis to be split.
- * svdq_i8_linear_forward: svdq_i8_quantize_rows, then svdq_i8_gemm with Y of X's dtype; xq and
- *     x_scale are scratch of the sizes above.
+ * svdq_i8_linear_forward: svdq_i8_quantize_rows, then svdq_i8_gemm with Y of X's dtype: the same bits.
+ *     xq and x_scale are scratch of the sizes above, with no defined contents afterwards (few tokens
+ *     are quantized where they are multiplied).
  * Asynchronous on stream. */
 SVDQ_API svdq_status svdq_i8_quantize_rows(const void *X, size_t x_stride, int dtype, int M, int K,
                                            const float *col_scale, int8_t *xq, float *x_scale, void *stream);
@@ -428,8 +429,9 @@ SVDQ_API svdq_status svdq_rope_axes_table(const svdq_positions *pos, int M, cons
  *   (u0, u1) -> (u0 cos - u1 sin, u1 cos + u0 sin) for every pair; with inverse the angle is negated,
  *   which undoes the rotation and is its gradient. Columns from 2 P on are copied.
  *   q, k        inputs (k NULL: Q alone), of dtype; heads and strides may differ (shared K heads).
- *   q_out, k_out  outputs, the same number of heads; may be the inputs themselves (same strides).
- * head_dim even, 2 P <= head_dim <= 512; at most 65536 heads; strides >= head_dim. Asynchronous on stream. */
+ *   q_out, k_out  outputs, the same number of heads; may be the inputs themselves (same strides). The
+ *               heads of an output must not overlap; those of an input may (stride 0: shared heads).
+ * head_dim even, 2 P <= head_dim <= 512; at most 65536 heads. Asynchronous on stream. */
 SVDQ_API svdq_status svdq_rope_axes_apply(const svdq_heads *q, const svdq_heads *q_out, const svdq_heads *k,
                                           const svdq_heads *k_out, int dtype, int M, int head_dim,
                                           const svdq_positions *pos, const svdq_rope_axes *axes, int inverse,

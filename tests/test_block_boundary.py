@@ -141,8 +141,10 @@ INVALID_ARGS = [
                                                               "theta=float('inf')", "theta=float('nan')", "shared_ladder=2", "halves=-1")],
     *[(c, dict(pos=a)) for c in ("_table", "_apply") for a in ("data=None", "dtype=0", "dtype=1", "dtype=7")],
     ("_apply", dict(D=63)), ("_apply", dict(D=62)), ("_apply", dict(D=0)), ("_apply", dict(D=1024)), ("_apply", dict(inverse=2)),
-    *[("_apply", {p: a}) for p in ("q", "qo", "k", "ko") for a in ("heads=0", "heads=3", "data=None", "token_stride=63", "head_stride=8",
-                                                                "heads=10**6")],
+    *[("_apply", {p: a}) for p in ("q", "qo", "k", "ko") for a in ("heads=0", "heads=3", "data=None", "heads=10**6")],
+    # outputs whose heads overlap
+    *[("_apply", {p: a}) for p in ("qo", "ko") for a in ("token_stride=63", "head_stride=8", "token_stride=0", "head_stride=0",
+                                                        "token_stride=64", "token_stride=100,head_stride=100")],
 ]
 
 
@@ -183,7 +185,9 @@ def test_valid_calls_reach_the_architecture_check(lib, unsupported):
                 ("_norm", dict(af=_affine(weight=None, bias=None, weight_stride=0))), ("_norm", dict(M=0, X=None, Y=None)),
                 ("_backward", dict(dw=None, db=None, ws=None, wsb=0)), ("_backward", dict(dX=None)), ("_backward", dict(af=None)),
                 ("_quantize", dict(col=None)), ("_quantize", dict(M=0, X=None, xq=None, s=None)), ("_gemm", dict(bias=None)),
-                ("_linear", dict(col=DEV, bias=DEV)), ("_apply", dict(k=None, ko=None)), ("_apply", dict(M=1, pos=_pos(token_stride=0))),
+                ("_linear", dict(col=DEV, bias=DEV)), ("_apply", dict(k=None, ko=None)),
+                ("_apply", dict(q=_h(head_stride=0), k=_h(heads=2, token_stride=0, head_stride=0))),
+                ("_apply", dict(qo=_h(token_stride=64, head_stride=6400), ko=_h(heads=2, token_stride=64, head_stride=6400))), ("_apply", dict(M=1, pos=_pos(token_stride=0))),
                 ("_table", dict(axes=_axes(n_axes=4, pairs=(64, 64, 64, 64))))]
     for name, kw in optional:
         assert CALLS[name](lib, **kw) == UNSUPPORTED, (name, kw)

@@ -66,6 +66,26 @@ def test_quantize_ties_zeros_and_extremes(dtype):
     assert bool(Y[6:].isnan().all()) and not bool(Y[2].any()) and bool(Y[:4].isfinite().all())
 
 
+@pytest.mark.parametrize("dtype,bits", [(BF16, 8), (F16, 11)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_quantize_every_16_bit_quotient(dtype, bits, wide):
+    """Every significand of a maximum with every value of the eight binades below it (whose quotients reach 1/2),
+    positive and negative: all borders that 16-bit values can come near to, and all ties. As 32-bit rows too."""
+    svdq = _svdq()
+    n = 2 ** (bits - 1)
+    sig = torch.arange(n, 2 * n, device="cuda").float() / n
+    values = torch.cat([sig * 2.0 ** -e for e in range(9)])  # n values in each of [1, 2), [1/2, 1), ..
+    for top in sig.split(128):
+        X = torch.minimum(values[None], top[:, None])  # what is above the maximum becomes it
+        X = torch.cat([X, -X], 1)
+        X = torch.nn.functional.pad(X, (0, -X.shape[1] % 16)).to(F32 if wide else dtype)
+        for part in X.split(4096, 1):
+            part = torch.cat([part, top[:, None].to(part.dtype), torch.zeros(len(top), 15, device="cuda", dtype=part.dtype)], 1)
+            xq, scale = svdq.i8_quantize_rows(part)
+            q, s = R.quantize_rows(part)
+            assert torch.equal(xq, q) and torch.equal(scale, s)
+
+
 @pytest.mark.parametrize("dtype", R.FLOATS)
 @pytest.mark.parametrize("K,at,wide", [(512, 1, 515), (64, 3, 100), (1040, 8, 2096)])
 def test_quantize_strided_rows(dtype, K, at, wide):

@@ -160,3 +160,14 @@ def test_special_values_pass_through():
     assert bool(bad[0, 0, 4:6].all()) and bool(bad[2, 1, 40]) and int(bad.sum()) <= 3
     y = y.float().nan_to_num(0.0, 0.0, 0.0)
     assert not bool(y.any())
+
+
+@pytest.mark.parametrize("dtype", R.FLOATS)
+def test_shared_heads_of_an_input(dtype):
+    """A head given for several by expansion (stride 0): each output is that head's."""
+    svdq = _svdq()
+    q = _normal(7, 1, 64, seed=14, dtype=dtype)
+    pos, axes = _pos(7, 1, 15), svdq.RopeAxes((32,))
+    want, _ = svdq.rope_axes_apply(q, None, pos, axes)
+    got, k = svdq.rope_axes_apply(q.expand(7, 5, 64), q.expand(7, 3, 64), pos.expand(7, 1), axes)
+    assert torch.equal(got, want.expand(7, 5, 64)) and torch.equal(k, want.expand(7, 3, 64))
