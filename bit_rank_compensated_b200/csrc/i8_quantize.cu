@@ -9,10 +9,9 @@ namespace svdq {
 namespace {
 
 // Rows in flight, and threads on an SM (registers for the row and its smoothing).
-template <typename T>
-constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+constexpr int kDepth = 2;
 template <typename T, int TEAM, int VEC, int E, bool FULL>
-using Ahead = RowsAhead<T, TEAM, VEC, E, FULL, kDepth<T>>;
+using Ahead = RowsAhead<T, TEAM, VEC, E, FULL, kDepth>;
 constexpr int kQuantThreads = 1024;
 
 template <typename T, int TEAM, int E, int VEC, bool FULL>
@@ -28,7 +27,7 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
   extern __shared__ __align__(16) uint8_t ring[];
   Ahead<T, TEAM, VEC, E, FULL> ahead;
 #pragma unroll
-  for (int d = 0; d < kDepth<T>; ++d) {
+  for (int d = 0; d < kDepth; ++d) {
     ahead.start(ring, d, x0, a.x_stride, m0, m1, a.K);
     copies_commit();
   }
@@ -42,7 +41,7 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
   int slot = 0;
   for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2];
-    copies_wait<kDepth<T> - 1>();
+    copies_wait<kDepth - 1>();
     ahead.take(slot, a.K, x);
     if (a.col_scale) {
 #pragma unroll
@@ -51,7 +50,7 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kQuantThreads)) k_qu
     const uint32_t most = top(thread_top(x), turn);
     ahead.refill(slot, x0, a.x_stride, m, m1, a.K);
     copies_commit();
-    slot = slot + 1 == kDepth<T> ? 0 : slot + 1;
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
     if (sizeof(T) == 2 && !a.col_scale) write.template operator()<true>(m, x, most);
     else write.template operator()<false>(m, x, most);
   }

@@ -20,11 +20,10 @@
 namespace svdq {
 namespace {
 
-// Rows in flight.
-template <typename T>
-constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+// Rows in flight a block (two, three and four: 27.5, 28.4 and 28.6 us for 9216 x 4096 of bf16).
+constexpr int kDepth = 2;
 template <typename T, int TEAM, int VEC, int E, bool FULL>
-using Ahead = RowsAhead<T, TEAM, VEC, E, FULL, kDepth<T>>;
+using Ahead = RowsAhead<T, TEAM, VEC, E, FULL, kDepth>;
 
 // Threads on an SM: registers for the row, its weight and bias; a row of 1024 threads has too few for
 // that and reads its weights again for every row (from L1).
@@ -49,7 +48,7 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
   extern __shared__ __align__(16) uint8_t ring[];
   Ahead<T, TEAM, VEC, E, FULL> ahead;
 #pragma unroll
-  for (int d = 0; d < kDepth<T>; ++d) {
+  for (int d = 0; d < kDepth; ++d) {
     ahead.start(ring, d, x0, a.x_stride, m0, m1, a.K);
     copies_commit();
   }
@@ -64,7 +63,7 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
   int slot = 0;
   for (int64_t m = m0; m < m1; ++m) {
     f32x2 x[E / 2];
-    copies_wait<kDepth<T> - 1>();
+    copies_wait<kDepth - 1>();
     ahead.take(slot, a.K, x);
     if (m >= group_end || !kKeepParams<TEAM>) {
       const size_t group = static_cast<uint32_t>(m) / static_cast<uint32_t>(a.rows_per_group);
@@ -76,7 +75,7 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kForwardThreads<TEAM
     sum(v, turn);
     ahead.refill(slot, x0, a.x_stride, m, m1, a.K);
     copies_commit();
-    slot = slot + 1 == kDepth<T> ? 0 : slot + 1;
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
     const float mean = v[0] * inv_k;
     const f32x2 minus = both(-mean);
     within_row<TEAM, VEC, E, FULL>(a.K, x, [&](f32x2 p, int) { return add2(p, minus); });

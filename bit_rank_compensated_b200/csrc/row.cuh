@@ -163,9 +163,8 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // The block's rows on their way: DEPTH of them in flight in a ring in shared memory, each thread's vectors
-// in slots of its own (asynchronous copies: neither registers nor barriers). 32 to 48 KiB in flight on an
-// SM is what the memory's latency wants; registers for two rows ahead gave less than that. Rows without
-// vectors (VEC = 1) are fetched one ahead, into registers.
+// in slots of its own (asynchronous copies: neither registers nor barriers). Rows without vectors (VEC = 1)
+// are fetched one ahead, into registers.
 template <typename T, int TEAM, int VEC, int E, bool FULL, int DEPTH>
 struct RowsAhead {
   static constexpr int NV = E / VEC;

@@ -198,3 +198,32 @@ def test_workspace_sizes(lib):
     assert lib.svdq_layer_norm_workspace_bytes(0, 64, 1, 1) == 0 and lib.svdq_layer_norm_workspace_bytes(8, 1 << 20, 1, 8) == 0
     for M, N, K in ((1, 4096, 4096), (77, 272, 8192), (4608, 12288, 4096)):
         assert lib.svdq_i8_workspace_bytes(M, N, K) % 16 == 0
+
+
+def test_calls_fail_loudly_without_the_compiled_binding(lib, monkeypatch):
+    import sys
+
+    import bit_rank_compensated_b200 as package
+    import torch
+    from bit_rank_compensated_b200 import svdq
+
+    monkeypatch.setattr(svdq, "_binding", None)
+    monkeypatch.delattr(package, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, "bit_rank_compensated_b200._binding", None)
+    with pytest.raises(RuntimeError, match="_binding.so"):
+        svdq.layer_norm(torch.zeros(2, 2))
+
+
+def test_host_tensors_are_refused(lib):
+    import torch
+    from bit_rank_compensated_b200 import svdq
+
+    x, q = torch.zeros(4, 32), torch.zeros(4, 2, 16)
+    i8, one = torch.zeros(4, 32, dtype=torch.int8), torch.ones(4)
+    axes = svdq.RopeAxes((4, 4))
+    for f in (lambda: svdq.layer_norm(x), lambda: svdq.layer_norm_backward(x, x, one, one), lambda: svdq.i8_quantize_rows(x),
+              lambda: svdq.i8_layer_norm_quantize(x), lambda: svdq.i8_gemm(i8, one, i8, one), lambda: svdq.i8_linear_forward(x, i8, one),
+              lambda: svdq.rope_axes_table(torch.zeros(4, 2), axes), lambda: svdq.rope_axes_apply(q, None, torch.zeros(4, 2), axes),
+              lambda: svdq.layer_norm(None), lambda: svdq.RopeAxes((0,)), lambda: svdq.RopeAxes((300,))):
+        with pytest.raises(ValueError):
+            f()
