@@ -193,12 +193,17 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
   } else if (warp >= EPI_WARP0) {
     // ------------------------------------------------------------ output stage
     const int group = (warp - EPI_WARP0) >> 2, quad = warp & 3;
-    const int row = quad * 32 + lane;
     const int et = (static_cast<int>(threadIdx.x) - EPI_WARP0 * 32) & 127;  // thread of the group
+    // This thread's elements of a 16-row, 8-column block: rows lane / 4 and 8 further, columns 2 (lane % 4) and
+    // the next (the 16x256b loads' layout). A thread so needs the scales of a quarter of the columns and of
+    // four rows; with a row to a thread the scales' way from shared memory (every thread all of them) took
+    // most of the output stage's time.
+    const int row = quad * 32 + lane / 4, col = 2 * (lane % 4);
     const uint32_t tlane = static_cast<uint32_t>(quad * 32) << 16;
     constexpr bool RAW = std::is_same_v<T, int>;
     constexpr int PER_BOX = 128 / sizeof(T);  // columns of a box
-    uint8_t *rowp = box_s + group * BOX_BYTES + row * 128;
+    constexpr int BLOCKS = PER_BOX / 8;       // 8-column blocks of a box
+    // shared addresses: the pointers' state space is lost in their alignment, and generic accesses are slower
     const uint32_t box = smem_u32(box_s + group * BOX_BYTES);
     bool ok = true;
     uint32_t n = 0;
@@ -209,11 +214,16 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
       const int n0 = (o / a.Mt) * BN + group * COLS;
       // this tile's scales and bias: the other parity's copy may still be read by the group's slower warps
       float *ws = scale_s + b * 2 * BN + group * COLS, *bs = ws + BN;
-      if (!RAW && et < COLS) {
-        ws[et] = n0 + et < a.N ? __ldg(a.w_scale + n0 + et) : 0.0f;
-        bs[et] = a.bias && n0 + et < a.N ? __ldg(a.bias + n0 + et) : 0.0f;
+      float xs[4] = {};
+      if constexpr (!RAW) {
+        if (et < COLS) {
+          ws[et] = n0 + et < a.N ? __ldg(a.w_scale + n0 + et) : 0.0f;
+          bs[et] = a.bias && n0 + et < a.N ? __ldg(a.bias + n0 + et) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xs[i] = row0 + row + 8 * i < a.M ? __ldg(a.x_scale + row0 + row + 8 * i) : 0.0f;
       }
-      const float xs = !RAW && row0 + row < a.M ? __ldg(a.x_scale + row0 + row) : 0.0f;
+      const uint32_t scales = smem_u32(ws) + 4 * col;
       named_bar_sync(1 + group, 128);
       if (ok) ok = mbar_wait_parked(bar_accfull + 8 * b, (n >> 1) & 1, a.err, KID_I8, 6);
       ok = __all_sync(0xffffffffu, ok);
@@ -221,50 +231,66 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
       const uint32_t taddr = tbase + tlane + b * BN + group * COLS;
 #pragma unroll 1
       for (int c = 0; c < COLS; c += PER_BOX) {
-        // the box is free once the copy unit has read it
-        if (et == 0) bulk_wait_read0();
-        named_bar_sync(1 + group, 128);
+        // the box's words: scaled, rounded and packed before the box has to be free
+        uint32_t w[2][2][BLOCKS][sizeof(T) / 2];  // [16 rows][8 rows][block][word]
+        float2 ws2[BLOCKS], bs2[BLOCKS];
+        if constexpr (!RAW) {
 #pragma unroll
-        for (int h = 0; h < PER_BOX; h += 32) {
-          uint32_t r[32];
-          if (ok) {
-            tmem_ld32(taddr + c + h, r);
-            tmem_wait_ld_dep(r);
+          for (int j = 0; j < BLOCKS; ++j) {
+            ws2[j] = ld_shared_f32x2(scales + 4 * (c + 8 * j));
+            bs2[j] = ld_shared_f32x2(scales + 4 * (BN + c + 8 * j));
           }
-          if (c + h + 32 == COLS) {
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[4 * BLOCKS];
+          if (ok) tmem_ld_16x256b(taddr + (static_cast<uint32_t>(16 * half) << 16) + c, r);
+          if (half == 1 && c + PER_BOX == COLS) {
             // the sums are in registers: the accumulator goes back to the MMAs
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(map_shared_rank(bar_accempty + 8 * b, 0));
           }
-          constexpr int PER16 = 16 / sizeof(T);  // columns per 16 bytes
 #pragma unroll
-          for (int q = 0; q < 32 / PER16; ++q) {
-            uint32_t w[4];
-            if constexpr (RAW) {
+          for (int j = 0; j < BLOCKS; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = r[q * 4 + e];
-            } else {
-              float v[PER16];
-#pragma unroll
-              for (int e = 0; e < PER16; e += 4) {
-                const float4 w4 = *reinterpret_cast<const float4 *>(ws + c + h + q * PER16 + e);
-                const float4 b4 = *reinterpret_cast<const float4 *>(bs + c + h + q * PER16 + e);
-                v[e] = scaled(static_cast<int>(r[q * PER16 + e]), xs, w4.x, b4.x);
-                v[e + 1] = scaled(static_cast<int>(r[q * PER16 + e + 1]), xs, w4.y, b4.y);
-                v[e + 2] = scaled(static_cast<int>(r[q * PER16 + e + 2]), xs, w4.z, b4.z);
-                v[e + 3] = scaled(static_cast<int>(r[q * PER16 + e + 3]), xs, w4.w, b4.w);
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(v[e]);
-                else w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t r0 = r[4 * j + 2 * i], r1 = r[4 * j + 2 * i + 1];
+              if constexpr (RAW) {
+                w[half][i][j][0] = r0;
+                w[half][i][j][1] = r1;
+              } else {
+                const float v0 = scaled(static_cast<int>(r0), xs[2 * half + i], ws2[j].x, bs2[j].x);
+                const float v1 = scaled(static_cast<int>(r1), xs[2 * half + i], ws2[j].y, bs2[j].y);
+                if constexpr (sizeof(T) == 4) {
+                  w[half][i][j][0] = __float_as_uint(v0);
+                  w[half][i][j][1] = __float_as_uint(v1);
+                } else {
+                  w[half][i][j][0] = pack2<T>(v0, v1);
+                }
               }
             }
-            const int ch = h / PER16 + q;
-            *reinterpret_cast<uint4 *>(rowp + ((ch ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
         }
+        // the box is free once the copy unit has read it
+        if (et == 0) bulk_wait_read0();
+        named_bar_sync(1 + group, 128);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rw = row + 16 * half + 8 * i;
+            const uint32_t at = box + rw * 128;
+#pragma unroll
+            for (int j = 0; j < BLOCKS; ++j) {
+              // 16-byte chunk k of a row lies at k ^ (row % 8)
+              if constexpr (sizeof(T) == 4) {
+                const int k = 2 * j + (lane % 4) / 2;
+                st_shared_u32x2(at + ((k ^ (rw & 7)) << 4) + 8 * (lane % 2), w[half][i][j][0], w[half][i][j][1]);
+              } else {
+                st_shared_u32(at + ((j ^ (rw & 7)) << 4) + 4 * (lane % 4), w[half][i][j][0]);
+              }
+            }
+          }
         fence_proxy_async_smem();
         named_bar_sync(1 + group, 128);
         if (et == 0) {
