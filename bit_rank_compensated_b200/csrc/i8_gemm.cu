@@ -21,8 +21,8 @@
 //
 // Warp roles (384 threads): warp 0 TMA producer; warp 1 tensor-memory owner and, in the even CTA, MMA
 // issuer; warps 2, 3 idle; warps 4..11 output stage, two groups of four warps, each 128 of the tile's
-// columns. An output thread owns a row (32 lanes per warp and sub-partition), scales it, rounds once, and
-// writes 128-byte rows of a swizzled box that a TMA store clips to M and N. Every wait is bounded.
+// columns. An output thread scales its share of 16 x 8 blocks, rounds once and writes to one of two swizzled
+// boxes, in turn, which TMA stores clip to M and N. Every wait is bounded.
 #include <type_traits>
 
 #include "block.h"
@@ -40,14 +40,14 @@ constexpr int GROUPS = 2;  // output groups of four warps
 constexpr int COLS = BN / GROUPS;  // columns of a group
 constexpr int THREADS = 32 * EPI_WARP0 + 128 * GROUPS;
 constexpr int ST = 5;  // stages
+constexpr int BOXES = 2;  // output boxes of a group
 constexpr uint32_t A_BYTES = BM * STEP;
 constexpr uint32_t B_BYTES = BN / 2 * STEP;
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr uint32_t BOX_BYTES = BM * 128;  // output box: 128 rows of 128 bytes
 constexpr uint32_t DATA_BYTES = ST * STAGE_BYTES;
-constexpr uint32_t SCALE_BYTES = 2 * 2 * BN * 4;  // w_scale and bias of the tile, two tiles
 constexpr int N_BARS = 2 * ST + 4;
-constexpr uint32_t SMEM = DATA_BYTES + GROUPS * BOX_BYTES + SCALE_BYTES + 256 + 1024;
+constexpr uint32_t SMEM = DATA_BYTES + GROUPS * BOXES * BOX_BYTES + 256 + 1024;
 constexpr uint32_t TMEM_COLS = 512;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 static_assert(N_BARS * 8 + 4 <= 256, "barrier area");
@@ -85,8 +85,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *box_s = smem + DATA_BYTES;
-  float *scale_s = reinterpret_cast<float *>(box_s + GROUPS * BOX_BYTES);  // [tile parity][w_scale, bias][BN]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(scale_s) + SCALE_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(box_s + GROUPS * BOXES * BOX_BYTES);
   // full[s] (even CTA): stage s is loaded in both CTAs; empty[s]: the MMAs that read it are done (both
   // CTAs); accfull[b]: accumulator b is complete (both CTAs); accempty[b] (even CTA): both CTAs have read it
   const uint32_t bar_full = smem_u32(bars), bar_empty = bar_full + 8 * ST;
@@ -204,7 +203,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     constexpr int PER_BOX = 128 / sizeof(T);  // columns of a box
     constexpr int BLOCKS = PER_BOX / 8;       // 8-column blocks of a box
     // shared addresses: the pointers' state space is lost in their alignment, and generic accesses are slower
-    const uint32_t box = smem_u32(box_s + group * BOX_BYTES);
+    const uint32_t boxes = smem_u32(box_s + group * BOXES * BOX_BYTES);
+    uint32_t turn = 0;  // boxes filled
     bool ok = true;
     uint32_t n = 0;
     for (int t = pid; t < tiles; t += npairs, ++n) {
@@ -212,35 +212,27 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
       const int o = t % mn;
       const int row0 = (o % a.Mt) * 2 * BM + static_cast<int>(crank) * BM;
       const int n0 = (o / a.Mt) * BN + group * COLS;
-      // this tile's scales and bias: the other parity's copy may still be read by the group's slower warps
-      float *ws = scale_s + b * 2 * BN + group * COLS, *bs = ws + BN;
+      // this thread's scales and bias, on their way while the MMAs run (N is even: a pair lies inside or outside)
       float xs[4] = {};
+      float2 ws2[COLS / 8], bs2[COLS / 8];
       if constexpr (!RAW) {
-        if (et < COLS) {
-          ws[et] = n0 + et < a.N ? __ldg(a.w_scale + n0 + et) : 0.0f;
-          bs[et] = a.bias && n0 + et < a.N ? __ldg(a.bias + n0 + et) : 0.0f;
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) xs[i] = row0 + row + 8 * i < a.M ? __ldg(a.x_scale + row0 + row + 8 * i) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < COLS / 8; ++j) {
+          const int nc = n0 + 8 * j + col;
+          ws2[j] = nc < a.N ? make_float2(__ldg(a.w_scale + nc), __ldg(a.w_scale + nc + 1)) : make_float2(0.0f, 0.0f);
+          bs2[j] = a.bias && nc < a.N ? make_float2(__ldg(a.bias + nc), __ldg(a.bias + nc + 1)) : make_float2(0.0f, 0.0f);
+        }
       }
-      const uint32_t scales = smem_u32(ws) + 4 * col;
-      named_bar_sync(1 + group, 128);
       if (ok) ok = mbar_wait_parked(bar_accfull + 8 * b, (n >> 1) & 1, a.err, KID_I8, 6);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const uint32_t taddr = tbase + tlane + b * BN + group * COLS;
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < COLS; c += PER_BOX) {
         // the box's words: scaled, rounded and packed before the box has to be free
         uint32_t w[2][2][BLOCKS][sizeof(T) / 2];  // [16 rows][8 rows][block][word]
-        float2 ws2[BLOCKS], bs2[BLOCKS];
-        if constexpr (!RAW) {
-#pragma unroll
-          for (int j = 0; j < BLOCKS; ++j) {
-            ws2[j] = ld_shared_f32x2(scales + 4 * (c + 8 * j));
-            bs2[j] = ld_shared_f32x2(scales + 4 * (BN + c + 8 * j));
-          }
-        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t r[4 * BLOCKS];
@@ -260,8 +252,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                 w[half][i][j][0] = r0;
                 w[half][i][j][1] = r1;
               } else {
-                const float v0 = scaled(static_cast<int>(r0), xs[2 * half + i], ws2[j].x, bs2[j].x);
-                const float v1 = scaled(static_cast<int>(r1), xs[2 * half + i], ws2[j].y, bs2[j].y);
+                const float v0 = scaled(static_cast<int>(r0), xs[2 * half + i], ws2[c / 8 + j].x, bs2[c / 8 + j].x);
+                const float v1 = scaled(static_cast<int>(r1), xs[2 * half + i], ws2[c / 8 + j].y, bs2[c / 8 + j].y);
                 if constexpr (sizeof(T) == 4) {
                   w[half][i][j][0] = __float_as_uint(v0);
                   w[half][i][j][1] = __float_as_uint(v1);
@@ -271,9 +263,10 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
               }
             }
         }
-        // the box is free once the copy unit has read it
-        if (et == 0) bulk_wait_read0();
+        // the box is free once the copy unit has read what it held two boxes ago
+        if (et == 0) bulk_wait_read1();
         named_bar_sync(1 + group, 128);
+        const uint32_t box = boxes + (turn++ & 1 ? BOX_BYTES : 0u);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
