@@ -14,8 +14,9 @@
 // What was measured: a step takes 0.28 us (550 cycles, 512 of them the MMAs') while the chip is not
 // full, and narrower tiles do not take less (256, 192, 128 and 64 channels: 13.4, 12.9, 12.8 and 13.4 us
 // for 16 tokens, 4096 x 4096, where they have as many steps), so there is one tile. Four output
-// groups (and four stages, for their boxes) instead of two cost 1.5 us a launch and 3 % of the large product;
-// two boxes a group (and four stages) gained 3 % where each pair has one tile and cost 2.4 % where it has many.
+// groups instead of two cost 1.5 us a launch and 3 % of the large product. The output stage takes 2850 cycles a
+// tile (4100 to 6200 with a row to a thread, which reads every scale; converting the sums by
+// integer arithmetic instead of the conversion instruction made it slower).
 // Where there are at most half as many tiles as pairs, the K axis is split: each pair writes the raw sums of its share and a second kernel
 // adds them (integers: in any order the same) and applies the scales.
 //
