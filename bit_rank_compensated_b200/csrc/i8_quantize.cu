@@ -79,7 +79,7 @@ cudaError_t quantize_t(const QuantRowsLaunch &a) {
   const bool vec = a.K % kVec<T> == 0 && rows_aligned(a.X, a.M > 1 ? a.x_stride : 0, sizeof(T), 16) &&
                    rows_aligned(a.col_scale, 0, 4, 16);
   return for_row(a.K, [&]<int TEAM, int E>() {
-    const int threads = row_threads(a.K, E);
+    const int threads = vec ? row_threads(a.K, E) : TEAM;
     const int blocks = a.num_sms * blocks_per_sm(threads, kQuantThreads);
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);

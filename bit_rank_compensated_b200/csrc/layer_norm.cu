@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(1024) k_layer_norm_slices(NormLaunch a, int sl
   float v = 0.0f;
   if (k < a.K) {
     const float *p = a.partial + (static_cast<size_t>(group) * slices * 2 + blockIdx.z) * a.K + k;
-#pragma unroll 4
-    for (int s = warp; s < n; s += 32) v += p[static_cast<size_t>(s) * 2 * a.K];
+#pragma unroll 16
+    for (int s = warp; s < n; s += 32) v += __ldcg(p + static_cast<size_t>(s) * 2 * a.K);
   }
   part[warp][lane] = v;
   __syncthreads();
@@ -233,11 +233,11 @@ template <typename T, bool QUANT>
 cudaError_t forward_t(const NormLaunch &a) {
   return for_row(a.K, [&]<int TEAM, int E>() {
     // a block's rows are consecutive: as many blocks as are resident at once
-    const int threads = row_threads(a.K, E);
+    const bool vec = vectors<T>(a);
+    const int threads = vec ? row_threads(a.K, E) : TEAM;
     const int blocks = a.num_sms * blocks_per_sm(threads, kForwardThreads<TEAM>);
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
-    const bool vec = vectors<T>(a);
     const int smem = vec ? Ahead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
     auto kern = !vec                 ? k_layer_norm<T, TEAM, E, 1, false, QUANT>
                 : row_full(a.K, E) ? k_layer_norm<T, TEAM, E, kVec<T>, true, QUANT>
@@ -286,7 +286,7 @@ cudaError_t backward_t(const NormLaunch &a) {
   const cudaError_t e = for_row(a.K, [&]<int TEAM, int E>() {
     const dim3 grid(static_cast<unsigned>(used) * s.slices);
     const bool vec = vectors<T>(a);
-    const int threads = row_threads(a.K, E);
+    const int threads = vec ? row_threads(a.K, E) : TEAM;
     const int smem = vec ? 2 * BackwardAhead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
     auto kern = !vec                 ? k_layer_norm_backward<T, TEAM, E, 1, false>
                 : row_full(a.K, E) ? k_layer_norm_backward<T, TEAM, E, kVec<T>, true>

@@ -3,9 +3,9 @@
 //
 // Thread t of a block of T <= TEAM threads holds E values as E / 2 pairs: VEC consecutive ones at columns
 // (v T + t) VEC, v = 0 .. E / VEC - 1, VEC values being 16 bytes (one load), or VEC = 1 where rows do not
-// start on 16 bytes or do not end on a whole vector (consecutive threads on consecutive columns). T is
-// the row's length over E, in whole warps; where that leaves nothing over (FULL), no column is checked.
-// Else columns from K on hold zeros.
+// start on 16 bytes or do not end on a whole vector (consecutive threads on consecutive columns). With vectors T
+// is the row's length over E, in whole warps; where that leaves nothing over (FULL), no column is checked.
+// Else columns from K on hold zeros. Without them T = TEAM, so that every value's offset is a constant.
 #pragma once
 
 #include <stdint.h>
@@ -22,7 +22,7 @@ constexpr int kVec = 16 / sizeof(T);
 
 template <int TEAM, int VEC>
 __device__ __forceinline__ int row_column(int i) {
-  const int t = TEAM == 32 ? 32 : static_cast<int>(blockDim.x);
+  const int t = TEAM == 32 || VEC == 1 ? TEAM : static_cast<int>(blockDim.x);
   return ((i / VEC) * t + static_cast<int>(threadIdx.x)) * VEC + i % VEC;
 }
 
@@ -107,19 +107,16 @@ __device__ __forceinline__ void within_row(int K, f32x2 (&x)[E / 2], F f) {
 template <int TEAM, int VEC, int E, bool FULL>
 __device__ __forceinline__ void load_params(const void *base, int dtype, size_t at, int K, float add, f32x2 (&w)[E / 2]) {
   if constexpr (VEC == 1) {
+    auto fill = [&](const auto *p) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      float f[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = row_column<TEAM, VEC>(2 * i + e);
-        f[e] = !FULL && k >= K      ? 0.0f
-               : dtype == SVDQ_F32 ? add + static_cast<const float *>(base)[at + k]
-               : dtype == SVDQ_F16 ? add + to_f32(static_cast<const __half *>(base)[at + k])
-                                   : add + to_f32(static_cast<const __nv_bfloat16 *>(base)[at + k]);
+      for (int i = 0; i < E / 2; ++i) {
+        const int k0 = row_column<TEAM, 1>(2 * i), k1 = row_column<TEAM, 1>(2 * i + 1);
+        w[i] = pair(k0 < K ? add + to_f32(p[k0]) : 0.0f, k1 < K ? add + to_f32(p[k1]) : 0.0f);
       }
-      w[i] = pair(f[0], f[1]);
-    }
+    };
+    if (dtype == SVDQ_F32) fill(static_cast<const float *>(base) + at);
+    else if (dtype == SVDQ_F16) fill(static_cast<const __half *>(base) + at);
+    else fill(static_cast<const __nv_bfloat16 *>(base) + at);
   } else {
     const f32x2 add_both = both(add);
 #pragma unroll
@@ -359,7 +356,7 @@ auto for_row(int K, F f) {
   if (K <= 8192) return f.template operator()<512, 16>();
   return f.template operator()<1024, 16>();
 }
-// Threads of a row's block, and whether they hold nothing but the row.
+// Threads of a row's block (with vectors), and whether they hold nothing but the row.
 inline int row_threads(int K, int E) { return ((K + E - 1) / E + 31) / 32 * 32; }
 inline bool row_full(int K, int E) { return K % (32 * E) == 0; }
 constexpr int kMaxRow = 16384;
