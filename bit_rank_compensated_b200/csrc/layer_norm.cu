@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k
       mean_n = a.mean[m + 1];
       rstd_n = a.rstd[m + 1];
     }
+    within_row<TEAM, VEC, E, FULL>(a.K, x, [&](f32x2 p, int) { return mul2(add2(p, minus), r2); });
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
-      x[i] = mul2(add2(x[i], minus), r2);  // a column from K on has g = 0
       dw[i] = fma2(g[i], x[i], dw[i]);
       db[i] = add2(db[i], g[i]);
       g[i] = mul2(g[i], w[i]);
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(1024) k_layer_norm_slices(NormLaunch a, int sl
   __shared__ float part[32][32];
   float *out = blockIdx.z == 0 ? a.dweight : a.dbias;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int k = blockIdx.x * 32 + lane;
-  const int group = blockIdx.y;
+  const int k = blockIdx.y * 32 + lane;
+  const int group = blockIdx.x;  // (there may be more groups than a grid has rows)
   const int64_t left = a.M - static_cast<int64_t>(group) * a.rows_per_group;
   const int rows = left <= 0 ? 0 : static_cast<int>(left < a.rows_per_group ? left : a.rows_per_group);
   const int n = (rows + chunk - 1) / chunk;  // slices that have rows
@@ -297,7 +297,7 @@ cudaError_t backward_t(const NormLaunch &a) {
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !sums || s.slices == 1) return e;
-  return launch_dependent(k_layer_norm_slices, dim3((a.K + 31) / 32, a.groups, 2), 1024, 0, a.stream, a, s.slices, s.chunk);
+  return launch_dependent(k_layer_norm_slices, dim3(a.groups, (a.K + 31) / 32, 2), 1024, 0, a.stream, a, s.slices, s.chunk);
 }
 
 }  // namespace

@@ -165,6 +165,34 @@ def test_backward_of_empty_groups():
     assert svdq.layer_norm(X[:0]).shape == (0, 320)
 
 
+def test_backward_of_many_groups_without_rows():
+    """More groups than a grid has rows, most of them behind the last row."""
+    svdq = _svdq()
+    X, w, _, _ = _inputs(1000, 40, 70000, 100, BF16, F32, 130)
+    dY = _normal(1000, 40, seed=134, dtype=BF16)
+    _, _, mean, rstd, _ = R.layer_norm(X, w, None, 100, 0.0)
+    mean, rstd = mean.float(), rstd.float()
+    _, dw, db = svdq.layer_norm_backward(dY, X, mean, rstd, w, rows_per_group=100)
+    want, bounds = R.layer_norm_backward(dY, X, mean, rstd, w[:10], 100, 10, 0.0)
+    R.assert_within(dw[:10], want[1], bounds[1] + 1e-30)
+    R.assert_within(db[:10], want[2], bounds[2] + 1e-30)
+    assert not bool(dw[10:].any()) and not bool(db[10:].any())
+
+
+@pytest.mark.parametrize("K", [96, 97, 100, 1000, 1024])
+def test_backward_of_far_constant_rows(K):
+    """mean * rstd overflows, x - mean does not: nothing of that comes from beside the row."""
+    svdq = _svdq()
+    X = torch.full((3, K), 1e35, device="cuda")
+    dY = _normal(3, K, seed=140)
+    mean, rstd = X[:, 0].clone(), torch.full((3,), 1e6, device="cuda")
+    dX, dw, db = svdq.layer_norm_backward(dY, X, mean, rstd)
+    want, bounds = R.layer_norm_backward(dY, X, mean, rstd, None, 3, 1, 0.0)
+    R.assert_within(dX, want[0], R.allowed(want[0], F32, bounds[0]))
+    assert not bool(dw.any())
+    R.assert_within(db, want[2], bounds[2] + 1e-30)
+
+
 def test_backward_against_differences():
     """dX, dweight and dbias against central differences of the forward pass in fp32."""
     svdq = _svdq()
