@@ -17,8 +17,8 @@
 // groups instead of two cost 1.5 us a launch and 3 % of the large product. The output stage takes 2850 cycles a
 // tile (4100 to 6200 with a row to a thread, which reads every scale; converting the sums by
 // integer arithmetic instead of the conversion instruction made it slower).
-// Where there are at most half as many tiles as pairs, the K axis is split: each pair writes the raw sums of its share and a second kernel
-// adds them (integers: in any order the same) and applies the scales.
+// Where there are at most half as many tiles as pairs, the K axis is split: each pair writes the raw sums of
+// its share and a second kernel adds them (integers: in any order the same) and applies the scales.
 //
 // Warp roles (384 threads): warp 0 TMA producer; warp 1 tensor-memory owner and, in the even CTA, MMA
 // issuer; warps 2, 3 idle; warps 4..11 output stage, two groups of four warps, each 128 of the tile's
