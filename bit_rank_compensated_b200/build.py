@@ -13,6 +13,7 @@ installed torch into bit_rank_compensated_b200/_binding.so.
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import glob
 import os
 import shutil
@@ -86,7 +87,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     hint = _cusolver_hint()
     defs = [f'-DSVDQ_CUSOLVER_HINT="{hint}"'] if hint else []
     hdr_t = _newest_header()
-    objs = []
+    objs, todo = [], []
     for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -95,7 +96,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *defs, *(extra_flags or []), "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        todo.append(cmd)
+    # the files do not depend on one another: a few compilers at a time
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as pool:
+        for _ in pool.map(lambda c: subprocess.run(c, check=True), todo):
+            pass
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc, *ARCH, "-shared", "-cudart=static", "-o", LIB, *objs, "-ldl", "-lpthread"]
         if verbose:
