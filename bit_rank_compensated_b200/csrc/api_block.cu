@@ -61,7 +61,7 @@ svdq_status norm_args(const void *X, size_t x_stride, int dtype, int M, int K, c
     a->bias_stride = af->bias_stride;
     a->param_dtype = af->dtype;
     a->groups = af->groups;
-    a->rows_per_group = af->rows_per_group;
+    a->rows_per_group = af->rows_per_group < a->rows_per_group ? af->rows_per_group : a->rows_per_group;  // the same groups
     a->weight_offset = af->weight_offset;
     if (!aligned(af->weight, elem_bytes(af->dtype)) || !aligned(af->bias, elem_bytes(af->dtype)))
       return SVDQ_ERR_MISALIGNED;
@@ -152,8 +152,8 @@ svdq_status svdq_layer_norm(const void *X, size_t x_stride, int dtype, int M, in
 }
 
 size_t svdq_layer_norm_workspace_bytes(int M, int K, int groups, int rows_per_group) {
-  if (M < 1 || K < 1 || K > kMaxNormColumns || groups < 1 || rows_per_group < 1) return 0;
-  return layer_norm_partial_bytes(M, K, rows_per_group);
+  if (M < 1 || M > kMaxRows || K < 1 || K > kMaxNormColumns || groups < 1 || rows_per_group < 1) return 0;
+  return layer_norm_partial_bytes(M, K, rows_per_group < M ? rows_per_group : M);
 }
 
 svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, const void *X, size_t x_stride, int dtype, int M,

@@ -258,33 +258,33 @@ cudaError_t forward(const NormLaunch &a) {
 // over all groups, but no slice of so few rows that its partial sums (8 bytes a column) would be more than
 // about half of what they are the sums of (three times a row's bytes).
 struct Slices {
+  int used;  // groups that have rows
   int slices, chunk;
 };
 Slices slices_of(int M, int K, int rows_per_group, int least) {
-  const int used = (M + rows_per_group - 1) / rows_per_group;
+  const int used = (M - 1) / rows_per_group + 1;  // (M + rows_per_group may pass 32 bits)
   const int rows = M < rows_per_group ? M : rows_per_group;
   const int threads = for_row(K, [K]<int TEAM, int E>() { return row_threads(K, E); });
   int s = 148 * blocks_per_sm(threads, kBackwardThreads) / used;
   if (s > (rows + least - 1) / least) s = (rows + least - 1) / least;
   if (s < 1) s = 1;
   const int chunk = (rows + s - 1) / s;
-  return {(rows + chunk - 1) / chunk, chunk};
+  return {used, (rows + chunk - 1) / chunk, chunk};
 }
 constexpr int least_rows(size_t elem_bytes) { return elem_bytes == 2 ? 3 : 2; }
 
 template <typename T>
 cudaError_t backward_t(const NormLaunch &a) {
   const Slices s = slices_of(a.M, a.K, a.rows_per_group, least_rows(sizeof(T)));
-  const int used = (a.M + a.rows_per_group - 1) / a.rows_per_group;
   const bool sums = a.dweight || a.dbias;
-  if (sums && s.slices == 1 && used < a.groups) {
+  if (sums && s.slices == 1 && s.used < a.groups) {
     // groups behind the last row (the second kernel zeroes them where there is one)
-    const size_t at = static_cast<size_t>(used) * a.K, bytes = static_cast<size_t>(a.groups - used) * a.K * 4;
+    const size_t at = static_cast<size_t>(s.used) * a.K, bytes = static_cast<size_t>(a.groups - s.used) * a.K * 4;
     if (a.dweight && cudaMemsetAsync(a.dweight + at, 0, bytes, a.stream) != cudaSuccess) return cudaErrorUnknown;
     if (a.dbias && cudaMemsetAsync(a.dbias + at, 0, bytes, a.stream) != cudaSuccess) return cudaErrorUnknown;
   }
   const cudaError_t e = for_row(a.K, [&]<int TEAM, int E>() {
-    const dim3 grid(static_cast<unsigned>(used) * s.slices);
+    const dim3 grid(static_cast<unsigned>(s.used) * s.slices);
     const bool vec = vectors<T>(a);
     const int threads = vec ? row_threads(a.K, E) : TEAM;
     const int smem = vec ? 2 * BackwardAhead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
@@ -310,8 +310,7 @@ size_t layer_norm_partial_bytes(int M, int K, int rows_per_group) {
   // enough for any type: fp32 rows make the shortest slices
   const Slices s = slices_of(M, K, rows_per_group, least_rows(4));
   if (s.slices == 1) return 0;
-  const size_t used = (static_cast<size_t>(M) + rows_per_group - 1) / rows_per_group;
-  return (used * s.slices * 2 * K * sizeof(float) + 15) / 16 * 16;
+  return (static_cast<size_t>(s.used) * s.slices * 2 * K * sizeof(float) + 15) / 16 * 16;
 }
 
 cudaError_t launch_layer_norm_backward(const NormLaunch &a) {
