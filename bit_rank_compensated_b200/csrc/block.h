@@ -93,15 +93,17 @@ struct RopeLaunch {
 cudaError_t launch_rope_table(const RopeLaunch &a);
 cudaError_t launch_rope_apply(const RopeLaunch &a);
 
-// Lets a kernel have `bytes` of dynamic shared memory on the current device. The attribute costs the host
-// some 3 us, so what a thread has set is remembered (a slot per kernel and device, lost to another one at
-// worst: setting it again is harmless).
-template <typename... Args>
-cudaError_t allow_smem(void (*kern)(Args...), int bytes) {
-  if (bytes <= 40 * 1024) return cudaSuccess;  // within the default, static arrays included
+// Lets a kernel have up to MOST bytes of dynamic shared memory on the current device: the most that any launch
+// of it takes, never one call's. The attribute belongs to the process, and what a thread sets replaces what another
+// one did, so that a smaller call would take from a larger one; with one value setting it again is harmless.
+// It costs the host some 3 us, so a thread remembers what it has set (a slot per kernel and device, lost to another
+// one at worst).
+template <int MOST, typename... Args>
+cudaError_t allow_smem(void (*kern)(Args...)) {
+  if constexpr (MOST <= 40 * 1024) return cudaSuccess;  // within the default, static arrays included
   struct Granted {
     const void *kern;
-    int device, bytes;
+    int device;
   };
   static thread_local Granted slots[64];
   int device = 0;
@@ -109,9 +111,9 @@ cudaError_t allow_smem(void (*kern)(Args...), int bytes) {
   if (e != cudaSuccess) return e;
   const void *key = reinterpret_cast<const void *>(kern);
   Granted &s = slots[(reinterpret_cast<uintptr_t>(key) / 64 + static_cast<uintptr_t>(device) * 17) % 64];
-  if (s.kern == key && s.device == device && s.bytes >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) s = {key, device, bytes};
+  if (s.kern == key && s.device == device) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
+  if (e == cudaSuccess) s = {key, device};
   return e;
 }
 

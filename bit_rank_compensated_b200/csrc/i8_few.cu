@@ -199,7 +199,7 @@ cudaError_t launch_mt(FewArgs a, int num_sms, cudaStream_t st) {
   const int rounds = (a.tasks + resident * num_sms - 1) / (resident * num_sms);
   const dim3 grid((a.tasks + rounds - 1) / rounds);
   auto kern = k_i8_few<T, MT, QUANT>;
-  const cudaError_t e = allow_smem(kern, smem);
+  const cudaError_t e = allow_smem<kMaxCodes>(kern);
   return e != cudaSuccess ? e : launch_dependent(kern, grid, 32 * kWarps, smem, st, a);
 }
 

@@ -379,7 +379,7 @@ cudaError_t launch_t(const I8GemmLaunch &g) {
   if (!mapped) return cudaErrorInvalidValue;
   const GArgs a{g.x_scale, g.w_scale, g.bias, g.M, g.N, g.K, (g.M + 2 * BM - 1) / (2 * BM), (g.N + BN - 1) / BN, splits, each, g.dev->err};
   auto kern = splits > 1 ? k_i8_gemm<int> : k_i8_gemm<T>;
-  cudaError_t err = allow_smem(kern, SMEM);
+  cudaError_t err = allow_smem<SMEM>(kern);
   if (err != cudaSuccess) return err;
   const int64_t tiles = static_cast<int64_t>(a.Mt) * a.Nt * splits;
   const int slots = g.dev->num_sms / 2;

@@ -86,8 +86,9 @@ cudaError_t quantize_t(const QuantRowsLaunch &a) {
     auto kern = !vec                 ? k_quantize_rows<T, TEAM, E, 1, false>
                 : row_full(a.K, E) ? k_quantize_rows<T, TEAM, E, kVec<T>, true>
                                    : k_quantize_rows<T, TEAM, E, kVec<T>, false>;
-    const int smem = vec ? Ahead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
-    const cudaError_t e = allow_smem(kern, smem);
+    using Ring = Ahead<T, TEAM, kVec<T>, E, true>;
+    const int smem = vec ? Ring::bytes(threads) : 0;
+    const cudaError_t e = vec ? allow_smem<Ring::bytes(TEAM)>(kern) : cudaSuccess;
     return e != cudaSuccess ? e : launch_dependent(kern, grid, threads, smem, a.stream, a, rows);
   });
 }

@@ -238,11 +238,12 @@ cudaError_t forward_t(const NormLaunch &a) {
     const int blocks = a.num_sms * blocks_per_sm(threads, kForwardThreads<TEAM>);
     const int rows = (a.M + blocks - 1) / blocks;
     const dim3 grid((a.M + rows - 1) / rows);
-    const int smem = vec ? Ahead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
+    using Ring = Ahead<T, TEAM, kVec<T>, E, true>;
+    const int smem = vec ? Ring::bytes(threads) : 0;
     auto kern = !vec                 ? k_layer_norm<T, TEAM, E, 1, false, QUANT>
                 : row_full(a.K, E) ? k_layer_norm<T, TEAM, E, kVec<T>, true, QUANT>
                                    : k_layer_norm<T, TEAM, E, kVec<T>, false, QUANT>;
-    const cudaError_t e = allow_smem(kern, smem);
+    const cudaError_t e = vec ? allow_smem<Ring::bytes(TEAM)>(kern) : cudaSuccess;
     return e != cudaSuccess ? e : launch_dependent(kern, grid, threads, smem, a.stream, a, rows);
   });
 }
@@ -287,11 +288,12 @@ cudaError_t backward_t(const NormLaunch &a) {
     const dim3 grid(static_cast<unsigned>(s.used) * s.slices);
     const bool vec = vectors<T>(a);
     const int threads = vec ? row_threads(a.K, E) : TEAM;
-    const int smem = vec ? 2 * BackwardAhead<T, TEAM, kVec<T>, E, true>::bytes(threads) : 0;
+    using Ring = BackwardAhead<T, TEAM, kVec<T>, E, true>;
+    const int smem = vec ? 2 * Ring::bytes(threads) : 0;
     auto kern = !vec                 ? k_layer_norm_backward<T, TEAM, E, 1, false>
                 : row_full(a.K, E) ? k_layer_norm_backward<T, TEAM, E, kVec<T>, true>
                                    : k_layer_norm_backward<T, TEAM, E, kVec<T>, false>;
-    const cudaError_t e = allow_smem(kern, smem);
+    const cudaError_t e = vec ? allow_smem<2 * Ring::bytes(TEAM)>(kern) : cudaSuccess;
     if (e != cudaSuccess) return e;
     kern<<<grid, threads, smem, a.stream>>>(a, s.slices, s.chunk);
     return cudaGetLastError();

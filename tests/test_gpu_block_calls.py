@@ -50,3 +50,69 @@ def test_one_group_for_all_rows_whatever_its_size(M, rows):
     assert st == 0
     assert torch.equal(out[2:4], got[1]) and bool((out[:2] == 7).all()) and bool((out[4:] == 7).all())
     assert svdq.last_device_error() == 0
+
+
+# ---------------------------------------------------------------- host threads
+class Worker:
+    """A host thread that makes calls when it is told to."""
+
+    def __init__(self):
+        import concurrent.futures
+
+        self.pool = concurrent.futures.ThreadPoolExecutor(max_workers=1)
+
+    def __call__(self, f):
+        return self.pool.submit(f).result(timeout=120)
+
+
+def _norm_call(svdq, dtype, K):
+    X, w = _normal(9, K, seed=10, dtype=dtype), _normal(K, seed=11)
+    return lambda: [svdq.layer_norm(X, w, w)]
+
+
+def _int8_norm_call(svdq, dtype, K):
+    X, w = _normal(9, K, seed=12, dtype=dtype), _normal(K, seed=13)
+    return lambda: list(svdq.i8_layer_norm_quantize(X, w, w))
+
+
+def _gradient_call(svdq, dtype, K):
+    X, dY = _normal(9, K, seed=14, dtype=dtype), _normal(9, K, seed=15, dtype=dtype)
+    _, mean, rstd = svdq.layer_norm(X[:, :64].contiguous(), stats=True)
+    return lambda: list(svdq.layer_norm_backward(dY, X, mean, rstd))
+
+
+def _quantize_call(svdq, dtype, K):
+    X = _normal(9, K, seed=16, dtype=dtype)
+    return lambda: list(svdq.i8_quantize_rows(X))
+
+
+def _few_call(svdq, dtype, K):
+    X = _normal(7, K, seed=17, dtype=dtype)
+    wq, ws = svdq.i8_quantize_rows(_normal(64, K, seed=18, dtype=dtype))
+    return lambda: [svdq.i8_linear_forward(X, wq, ws)]
+
+
+@pytest.mark.parametrize("call,dtype,large,small", [
+    (_norm_call, F32, 16384, 12288), (_norm_call, F16, 16384, 12800), (_int8_norm_call, BF16, 16384, 12800),
+    (_gradient_call, BF16, 8192, 6144), (_gradient_call, F32, 8192, 6144), (_gradient_call, F16, 16384, 12288),
+    (_quantize_call, F32, 16384, 12288), (_few_call, BF16, 12288, 8192), (_few_call, F32, 12288, 8192),
+])
+def test_two_threads_with_rows_of_different_lengths(call, dtype, large, small):
+    """Two host threads use one kernel with more and with less shared memory in turn: neither takes from the other
+    what its launches need."""
+    svdq = _svdq()
+    a, b = Worker(), Worker()
+    more, less = call(svdq, dtype, large), call(svdq, dtype, small)
+    first = a(more)
+    for _ in range(3):
+        other = b(less)
+        for x, y in zip(a(more), first):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        for x, y in zip(b(less), other):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    # and both at once
+    futures = [w.pool.submit(lambda f=f: [f() for _ in range(20)]) for w, f in ((a, more), (b, less))]
+    for got in (f.result(timeout=120) for f in futures):
+        assert len(got) == 20
+    torch.cuda.synchronize()
+    assert svdq.last_device_error() == 0
