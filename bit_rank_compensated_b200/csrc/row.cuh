@@ -213,14 +213,14 @@ struct RowsAhead {
 
 template <typename T, int TEAM, int E, bool FULL, int DEPTH>
 struct RowsAhead<T, TEAM, 1, E, FULL, DEPTH> {
-  float next[E];
+  T next[E];  // as loaded: a conversion would wait for them
 
   static constexpr int bytes(int) { return 0; }
   __device__ __forceinline__ void fetch(const T *p, int K) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int k = row_column<TEAM, 1>(i);
-      next[i] = FULL || k < K ? to_f32(p[k]) : 0.0f;
+      next[i] = FULL || k < K ? p[k] : from_f32<T>(0.0f);
     }
   }
   __device__ __forceinline__ void start(uint8_t *, int d, const T *x0, size_t stride, int64_t m0, int64_t m1, int K) {
@@ -228,7 +228,7 @@ struct RowsAhead<T, TEAM, 1, E, FULL, DEPTH> {
   }
   __device__ __forceinline__ void take(int, int, f32x2 (&x)[E / 2]) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) x[i] = pair(next[2 * i], next[2 * i + 1]);
+    for (int i = 0; i < E / 2; ++i) x[i] = pair(to_f32(next[2 * i]), to_f32(next[2 * i + 1]));
   }
   __device__ __forceinline__ void refill(int, const T *x0, size_t stride, int64_t m, int64_t m1, int K) {
     if (m + 1 < m1) fetch(x0 + (m + 1) * stride, K);

@@ -116,3 +116,52 @@ def test_two_threads_with_rows_of_different_lengths(call, dtype, large, small):
         assert len(got) == 20
     torch.cuda.synchronize()
     assert svdq.last_device_error() == 0
+
+
+# ---------------------------------------------------------------- rows far from zero
+@pytest.mark.parametrize("dtype", R.FLOATS)
+@pytest.mark.parametrize("K", [3, 97, 104, 777, 1000, 1153, 1920, 4096, 5120, 12288, 16383])
+def test_a_constant_row_is_its_bias(K, dtype):
+    """x - mean is 0 for every column, whatever K and the value: no rounding of the mean is left for rstd = eps^-1/2
+    to make a thousand times larger. (The sum of K <= 16384 equal values is within 131 U of itself, so the first mean
+    is off by j <= 131 steps of the value; x less it is exact, K j < 2^24 steps sum exactly, and their mean is j.)"""
+    svdq = _svdq()
+    values = [0.0, 1.0, -3.0, 0.1, 100.0, 1000.0, -1000.1, 1 / 3, 3e4, 1e-3] + ([1e6, 7654321.0, 3e9, -1e-9] if dtype != F16 else [])
+    X = torch.tensor(values, device="cuda").to(dtype)[:, None].repeat(1, K)
+    w, b = _normal(K, seed=20), _normal(K, seed=21)
+    Y, mean, rstd = svdq.layer_norm(X, w, b, stats=True)
+    assert torch.equal(Y, b.to(dtype).expand_as(Y))
+    assert torch.equal(mean, X[:, 0].float())
+    # the variance is 0 in exact arithmetic; what is subtracted as the first mean's error squared leaves 4 U of it at
+    # most, beside eps
+    left = 4 * R.U * (131 * R.U * X[:, 0].double()) ** 2 * 140
+    assert bool(((rstd.double() * R.EPS ** 0.5 - 1).abs() <= 140 * R.U + left / R.EPS).all())
+    assert not bool(svdq.layer_norm(X).any())
+    if K % 16 == 0:
+        xq, scale = svdq.i8_layer_norm_quantize(X)
+        assert not bool(xq.any()) and not bool(scale.any())
+
+
+# rows, columns, mean, deviation
+FAR = [(5, 1920, 1000.0, 1e-2), (5, 777, 1000.0, 1.0), (3, 4096, -5e4, 1.0), (4, 1153, 30.0, 1e-3), (3, 12288, 300.0, 0.1),
+       (3, 104, 1e4, 1e-1), (2, 16384, 100.0, 1e-3)]
+
+
+@pytest.mark.parametrize("M,K,far,deviation", FAR)
+def test_rows_far_from_zero(M, K, far, deviation):
+    """With A = mean|x|: the first mean is within D = 131 U A; d = x - mean rounds once, its sum within 130 U sum|d|;
+    so x - mean is within 134 U (mean|d|) + 4 U |d| of itself, where |d| <= |x - mean| + D, and no longer within
+    130 U A. The variance is sum d^2 / K (140 U of it and of D^2) less the square of what was corrected."""
+    svdq = _svdq()
+    X = far + _normal(M, K, seed=30, scale=deviation)
+    x = X.double()
+    mu = x.mean(1, keepdim=True)
+    c = x - mu
+    rs = 1 / torch.sqrt((c * c).mean(1, keepdim=True) + R.EPS)
+    D = 131 * R.U * x.abs().mean(1, keepdim=True)
+    off = 134 * R.U * (c.abs().mean(1, keepdim=True) + D) + 4 * R.U * (c.abs() + D)
+    rel = 150 * R.U * (1 + (D * rs) ** 2)
+    Y, mean, rstd = svdq.layer_norm(X, stats=True)
+    R.assert_within(rstd[:, None], rs, rel * rs)
+    R.assert_within(mean[:, None], mu, off.amax(1, keepdim=True) + R.U * mu.abs())
+    R.assert_within(Y, c * rs, rs * off * (1 + rel) + (rel + 4 * R.U) * (c * rs).abs())
