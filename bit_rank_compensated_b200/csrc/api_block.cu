@@ -176,8 +176,8 @@ svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, const voi
   a.stream = static_cast<cudaStream_t>(stream);
   if (M == 0) {
     const size_t bytes = static_cast<size_t>(a.groups) * k * sizeof(float);
-    if (dweight && cudaMemsetAsync(dweight, 0, bytes, a.stream) != cudaSuccess) return SVDQ_ERR_CUDA;
-    if (dbias && cudaMemsetAsync(dbias, 0, bytes, a.stream) != cudaSuccess) return SVDQ_ERR_CUDA;
+    for (float *p : {dweight, dbias})
+      if (p && (st = done(reported(cudaMemsetAsync(p, 0, bytes, a.stream)))) != SVDQ_OK) return st;
     return SVDQ_OK;
   }
   if (!dX && !dweight && !dbias) return SVDQ_OK;

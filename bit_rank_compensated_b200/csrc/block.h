@@ -93,6 +93,13 @@ struct RopeLaunch {
 cudaError_t launch_rope_table(const RopeLaunch &a);
 cudaError_t launch_rope_apply(const RopeLaunch &a);
 
+// A call's error, on its way to the caller. The runtime keeps a failed call's error for whoever asks for the last one
+// next, which would be another call, whose own launch succeeded.
+inline cudaError_t reported(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // Lets a kernel have up to MOST bytes of dynamic shared memory on the current device: the most that any launch
 // of it takes, never one call's. The attribute belongs to the process, and what a thread sets replaces what another
 // one did, so that a smaller call would take from a larger one; with one value setting it again is harmless.
@@ -108,20 +115,19 @@ cudaError_t allow_smem(void (*kern)(Args...)) {
   static thread_local Granted slots[64];
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) return reported(e);
   const void *key = reinterpret_cast<const void *>(kern);
   Granted &s = slots[(reinterpret_cast<uintptr_t>(key) / 64 + static_cast<uintptr_t>(device) * 17) % 64];
   if (s.kern == key && s.device == device) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
+  e = cudaFuncSetAttribute(key, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
   if (e == cudaSuccess) s = {key, device};
-  return e;
+  return reported(e);
 }
 
-// Launches a kernel that waits (grid_dep_wait) before it touches global memory, so that its start may
-// overlap the end of the stream's previous kernel.
-template <typename... Args>
-cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                             std::type_identity_t<Args>... args) {
+// Launches a kernel, after the stream's previous one has ended or (DEPENDENT, below) before.
+template <bool DEPENDENT, typename... Args>
+cudaError_t launch_kernel(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                          std::type_identity_t<Args>... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
@@ -131,8 +137,19 @@ cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, size
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  cfg.numAttrs = DEPENDENT ? 1 : 0;
+  return reported(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+template <typename... Args>
+cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, std::type_identity_t<Args>... args) {
+  return launch_kernel<false>(kern, grid, threads, smem, st, args...);
+}
+// Of a kernel that waits (grid_dep_wait) before it touches global memory, so that its start may overlap the end of
+// the stream's previous kernel.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                             std::type_identity_t<Args>... args) {
+  return launch_kernel<true>(kern, grid, threads, smem, st, args...);
 }
 
 }  // namespace svdq

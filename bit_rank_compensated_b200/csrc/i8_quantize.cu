@@ -73,8 +73,7 @@ __global__ void __launch_bounds__(1024) k_quantize_long_rows(QuantRowsLaunch a) 
 template <typename T>
 cudaError_t quantize_t(const QuantRowsLaunch &a) {
   if (a.K > kMaxRow) {
-    k_quantize_long_rows<T><<<a.M, 1024, 0, a.stream>>>(a);
-    return cudaGetLastError();
+    return launch(k_quantize_long_rows<T>, dim3(a.M), 1024, 0, a.stream, a);
   }
   const bool vec = a.K % kVec<T> == 0 && rows_aligned(a.X, a.M > 1 ? a.x_stride : 0, sizeof(T), 16) &&
                    rows_aligned(a.col_scale, 0, 4, 16);

@@ -304,8 +304,10 @@ cudaError_t backward_t(const NormLaunch &a) {
   if (sums && s.slices == 1 && s.used < a.groups) {
     // groups behind the last row (the second kernel zeroes them where there is one)
     const size_t at = static_cast<size_t>(s.used) * a.K, bytes = static_cast<size_t>(a.groups - s.used) * a.K * 4;
-    if (a.dweight && cudaMemsetAsync(a.dweight + at, 0, bytes, a.stream) != cudaSuccess) return cudaErrorUnknown;
-    if (a.dbias && cudaMemsetAsync(a.dbias + at, 0, bytes, a.stream) != cudaSuccess) return cudaErrorUnknown;
+    for (float *p : {a.dweight, a.dbias}) {
+      const cudaError_t e = p ? reported(cudaMemsetAsync(p + at, 0, bytes, a.stream)) : cudaSuccess;
+      if (e != cudaSuccess) return e;
+    }
   }
   const cudaError_t e = for_row(a.K, [&]<int TEAM, int E>() {
     const dim3 grid(static_cast<unsigned>(s.used) * s.slices);
@@ -318,8 +320,7 @@ cudaError_t backward_t(const NormLaunch &a) {
                                    : k_layer_norm_backward<T, TEAM, E, kVec<T>, false>;
     const cudaError_t e = vec ? allow_smem<2 * Ring::bytes(TEAM)>(kern) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    kern<<<grid, threads, smem, a.stream>>>(a, s.slices, s.chunk);
-    return cudaGetLastError();
+    return launch(kern, grid, threads, smem, a.stream, a, s.slices, s.chunk);
   });
   if (e != cudaSuccess || !sums || s.slices == 1) return e;
   return launch_dependent(k_layer_norm_slices, dim3(a.groups, (a.K + 31) / 32, 2), 1024, 0, a.stream, a, s.slices, s.chunk);
