@@ -102,11 +102,11 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device &devic
   return at::empty(shape, at::TensorOptions().dtype(type).device(device));
 }
 
-// A caller's M x K output of a type, or a new one.
+// A caller's M x K output of a type, or none; its rows' distance either way.
 Tensor output(PyObject *o, const char *name, const Rows &r, const Tensor &like, size_t *stride) {
   if (!has(o)) {
     *stride = static_cast<size_t>(r.K);
-    return fresh({r.M, r.K}, like.scalar_type(), like.device());
+    return {};
   }
   const Tensor &t = tensor(o, name);
   const Rows q = rows_of(t, name);
@@ -127,6 +127,14 @@ float number(PyObject *o) {
   return static_cast<float>(v);
 }
 bool truth(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+
+// While a call allocates and launches, other threads may run Python: an allocation can be slow, and a launch can wait for a
+// full queue, whose next entry may be a host function that needs the interpreter. Nothing in its scope touches a
+// Python object.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 void *stream_of(const at::Device &d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
 
@@ -172,24 +180,26 @@ svdq_norm_affine affine_of(const Tensor &X, const Rows &r, PyObject *weight, PyO
   return a;
 }
 
-// A caller's workspace or a new one of `need` bytes.
+// A caller's workspace, or one of `need` bytes.
 struct Space {
   Tensor kept;
   void *data = nullptr;
   size_t bytes = 0;
+
+  void make(size_t need, const at::Device &device) {
+    if (!kept.defined() && need > 0) kept = fresh({static_cast<int64_t>(need)}, at::kByte, device);
+    if (kept.defined()) {
+      data = kept.data_ptr();
+      bytes = kept.nbytes();
+    }
+  }
 };
-Space space_of(PyObject *o, size_t need, const at::Device &device) {
+Space space_of(PyObject *o, const at::Device &device) {
   Space s;
   if (has(o)) {
     s.kept = tensor(o, "workspace");
     if (s.kept.device() != device || !s.kept.is_contiguous()) refuse("the workspace must be contiguous and on " + device.str());
-  } else if (need > 0) {
-    s.kept = fresh({static_cast<int64_t>(need)}, at::kByte, device);
-  } else {
-    return s;
   }
-  s.data = s.kept.data_ptr();
-  s.bytes = s.kept.nbytes();
   return s;
 }
 
@@ -210,21 +220,26 @@ PyObject *layer_norm(PyObject *const *a) {
   const Tensor &X = tensor(a[0], "X");
   const int code = float_code(X, "X");
   const Rows r = rows_of(X, "X");
+  const at::Device device = X.device();
   const svdq_norm_affine af = affine_of(X, r, a[1], a[2], integer(a[3]), number(a[4]), 0);
-  const c10::cuda::CUDAGuard guard(X.device());
+  const float eps = number(a[5]);
   size_t stride = 0;
-  const Tensor Y = output(a[6], "Y", r, X, &stride);
-  Tensor mean, rstd;
-  if (truth(a[7])) {
-    mean = fresh({r.M}, at::kFloat, X.device());
-    rstd = fresh({r.M}, at::kFloat, X.device());
+  Tensor Y = output(a[6], "Y", r, X, &stride), mean, rstd;
+  const bool stats = truth(a[7]);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(device);
+    if (!Y.defined()) Y = fresh({r.M, r.K}, X.scalar_type(), device);
+    if (stats) {
+      mean = fresh({r.M}, at::kFloat, device);
+      rstd = fresh({r.M}, at::kFloat, device);
+    }
+    st = entry.layer_norm(X.data_ptr(), r.stride, code, r.M, r.K, &af, eps, Y.data_ptr(), stride,
+                          stats ? mean.data_ptr<float>() : nullptr, stats ? rstd.data_ptr<float>() : nullptr, stream_of(device));
   }
-  const svdq_status st =
-      entry.layer_norm(X.data_ptr(), r.stride, code, r.M, r.K, &af, number(a[5]), Y.data_ptr(), stride,
-                       mean.defined() ? mean.data_ptr<float>() : nullptr, rstd.defined() ? rstd.data_ptr<float>() : nullptr,
-                       stream_of(X.device()));
   if (st != SVDQ_OK) return status(st);
-  return mean.defined() ? tuple({Y, mean, rstd}) : wrap(Y);
+  return stats ? tuple({Y, mean, rstd}) : wrap(Y);
 }
 
 // dY, X, mean, rstd, weight, rows_per_group, weight_offset, dX, groups, need_dX, need_dweight, need_dbias, workspace
@@ -242,18 +257,23 @@ PyObject *layer_norm_backward(PyObject *const *a) {
   const svdq_norm_affine af = affine_of(X, r, a[4], Py_None, integer(a[5]), number(a[6]), groups);
   if (!has(a[2]) || !has(a[3])) refuse("mean and rstd must be given");
   const float *mean = floats(a[2], "mean", r.M, device), *rstd = floats(a[3], "rstd", r.M, device);
-  const c10::cuda::CUDAGuard guard(device);
+  const bool need_dX = truth(a[9]), need_dw = truth(a[10]), need_db = truth(a[11]);
   size_t stride = static_cast<size_t>(r.K);
   Tensor dX, dw, db;
-  if (truth(a[9])) dX = output(a[7], "dX", r, X, &stride);
-  if (truth(a[10])) dw = fresh({af.groups, r.K}, at::kFloat, device);
-  if (truth(a[11])) db = fresh({af.groups, r.K}, at::kFloat, device);
-  const bool sums = dw.defined() || db.defined();
-  const Space s = space_of(a[12], sums ? entry.layer_norm_workspace_bytes(r.M, r.K, af.groups, af.rows_per_group) : 0, device);
-  const svdq_status st = entry.layer_norm_backward(
-      dY.data_ptr(), d.stride, X.data_ptr(), r.stride, code, r.M, r.K, &af, mean, rstd, dX.defined() ? dX.data_ptr() : nullptr,
-      stride, dw.defined() ? dw.data_ptr<float>() : nullptr, db.defined() ? db.data_ptr<float>() : nullptr, s.data, s.bytes,
-      stream_of(device));
+  if (need_dX) dX = output(a[7], "dX", r, X, &stride);
+  Space s = space_of(a[12], device);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(device);
+    if (need_dX && !dX.defined()) dX = fresh({r.M, r.K}, X.scalar_type(), device);
+    if (need_dw) dw = fresh({af.groups, r.K}, at::kFloat, device);
+    if (need_db) db = fresh({af.groups, r.K}, at::kFloat, device);
+    s.make(need_dw || need_db ? entry.layer_norm_workspace_bytes(r.M, r.K, af.groups, af.rows_per_group) : 0, device);
+    st = entry.layer_norm_backward(dY.data_ptr(), d.stride, X.data_ptr(), r.stride, code, r.M, r.K, &af, mean, rstd,
+                                   need_dX ? dX.data_ptr() : nullptr, stride, need_dw ? dw.data_ptr<float>() : nullptr,
+                                   need_db ? db.data_ptr<float>() : nullptr, s.data, s.bytes, stream_of(device));
+  }
   return st != SVDQ_OK ? status(st) : tuple({dX, dw, db});
 }
 
@@ -261,26 +281,26 @@ PyObject *layer_norm_backward(PyObject *const *a) {
 // Int8 rows and their scales: the caller's or new ones.
 struct I8Rows {
   Tensor xq, scale;
-  int8_t *q;
-  float *s;
+  int8_t *q = nullptr;
+  float *s = nullptr;
+
+  void make(const Rows &r, const at::Device &device) {
+    if (!xq.defined()) xq = fresh({r.M, r.K}, at::kChar, device);
+    if (!scale.defined()) scale = fresh({r.M}, at::kFloat, device);
+    q = static_cast<int8_t *>(xq.data_ptr());
+    s = static_cast<float *>(scale.data_ptr());
+  }
 };
 I8Rows i8_rows(PyObject *xq, PyObject *scale, const Rows &r, const at::Device &device) {
   I8Rows o;
-  const int64_t n = static_cast<int64_t>(r.M) * r.K;
   if (has(xq)) {
-    values(xq, "xq", n, at::kChar, device);
+    values(xq, "xq", static_cast<int64_t>(r.M) * r.K, at::kChar, device);
     o.xq = tensor(xq, "xq");
-  } else {
-    o.xq = fresh({r.M, r.K}, at::kChar, device);
   }
   if (has(scale)) {
     values(scale, "x_scale", r.M, at::kFloat, device);
     o.scale = tensor(scale, "x_scale");
-  } else {
-    o.scale = fresh({r.M}, at::kFloat, device);
   }
-  o.q = static_cast<int8_t *>(o.xq.data_ptr());
-  o.s = static_cast<float *>(o.scale.data_ptr());
   return o;
 }
 
@@ -289,10 +309,16 @@ PyObject *i8_quantize_rows(PyObject *const *a) {
   const Tensor &X = tensor(a[0], "X");
   const int code = float_code(X, "X");
   const Rows r = rows_of(X, "X");
-  const float *col = floats(a[1], "col_scale", r.K, X.device());
-  const c10::cuda::CUDAGuard guard(X.device());
-  const I8Rows o = i8_rows(a[2], a[3], r, X.device());
-  const svdq_status st = entry.i8_quantize_rows(X.data_ptr(), r.stride, code, r.M, r.K, col, o.q, o.s, stream_of(X.device()));
+  const at::Device device = X.device();
+  const float *col = floats(a[1], "col_scale", r.K, device);
+  I8Rows o = i8_rows(a[2], a[3], r, device);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(device);
+    o.make(r, device);
+    st = entry.i8_quantize_rows(X.data_ptr(), r.stride, code, r.M, r.K, col, o.q, o.s, stream_of(device));
+  }
   return st != SVDQ_OK ? status(st) : tuple({o.xq, o.scale});
 }
 
@@ -301,11 +327,17 @@ PyObject *i8_layer_norm_quantize(PyObject *const *a) {
   const Tensor &X = tensor(a[0], "X");
   const int code = float_code(X, "X");
   const Rows r = rows_of(X, "X");
+  const at::Device device = X.device();
   const svdq_norm_affine af = affine_of(X, r, a[1], a[2], integer(a[3]), number(a[4]), 0);
-  const c10::cuda::CUDAGuard guard(X.device());
-  const I8Rows o = i8_rows(a[6], a[7], r, X.device());
-  const svdq_status st =
-      entry.i8_layer_norm_quantize(X.data_ptr(), r.stride, code, r.M, r.K, &af, number(a[5]), o.q, o.s, stream_of(X.device()));
+  const float eps = number(a[5]);
+  I8Rows o = i8_rows(a[6], a[7], r, device);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(device);
+    o.make(r, device);
+    st = entry.i8_layer_norm_quantize(X.data_ptr(), r.stride, code, r.M, r.K, &af, eps, o.q, o.s, stream_of(device));
+  }
   return st != SVDQ_OK ? status(st) : tuple({o.xq, o.scale});
 }
 
@@ -325,8 +357,9 @@ I8Weight i8_weight(PyObject *wq, PyObject *scale, PyObject *bias, int K, const a
   o.bias = floats(bias, "bias", o.N, device);
   return o;
 }
+// A caller's product, or none.
 Tensor i8_output(PyObject *o, int M, int N, at::ScalarType type, const at::Device &device) {
-  if (!has(o)) return fresh({M, N}, type, device);
+  if (!has(o)) return {};
   values(o, "Y", static_cast<int64_t>(M) * N, type, device);
   return tensor(o, "Y");
 }
@@ -342,10 +375,16 @@ PyObject *i8_gemm(PyObject *const *a) {
   const I8Weight w = i8_weight(a[2], a[3], a[4], r.K, device);
   const int code = static_cast<int>(integer(a[6]));
   const at::ScalarType type = code == SVDQ_BF16 ? at::kBFloat16 : (code == SVDQ_F16 ? at::kHalf : at::kFloat);
-  const c10::cuda::CUDAGuard guard(device);
-  const Tensor Y = i8_output(a[5], r.M, w.N, type, device);
-  const Space s = space_of(a[7], entry.i8_workspace_bytes(r.M, w.N, r.K), device);
-  const svdq_status st = entry.i8_gemm(x, xs, r.M, w.wq, w.scale, w.bias, w.N, r.K, Y.data_ptr(), code, s.data, s.bytes, stream_of(device));
+  Tensor Y = i8_output(a[5], r.M, w.N, type, device);
+  Space s = space_of(a[7], device);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(device);
+    if (!Y.defined()) Y = fresh({r.M, w.N}, type, device);
+    s.make(entry.i8_workspace_bytes(r.M, w.N, r.K), device);
+    st = entry.i8_gemm(x, xs, r.M, w.wq, w.scale, w.bias, w.N, r.K, Y.data_ptr(), code, s.data, s.bytes, stream_of(device));
+  }
   return st != SVDQ_OK ? status(st) : wrap(Y);
 }
 
@@ -357,25 +396,31 @@ PyObject *i8_linear_forward(PyObject *const *a) {
   const at::Device device = X.device();
   const I8Weight w = i8_weight(a[1], a[2], a[3], r.K, device);
   const float *col = floats(a[4], "col_scale", r.K, device);
-  const c10::cuda::CUDAGuard guard(device);
-  const Tensor Y = i8_output(a[7], r.M, w.N, X.scalar_type(), device);
-  const size_t need = entry.i8_workspace_bytes(r.M, w.N, r.K);
-  I8Rows x;
-  Space s;
-  if (!has(a[5]) && !has(a[6]) && !has(a[8])) {
-    // scratch in one piece: the rows (16-byte multiples, or the library refuses K), the workspace, the scales
-    const size_t n = (static_cast<size_t>(r.M) * r.K + 15) / 16 * 16;
-    s.kept = fresh({static_cast<int64_t>(n + need + 4 * static_cast<size_t>(r.M))}, at::kChar, device);
-    x.q = static_cast<int8_t *>(s.kept.data_ptr());
-    x.s = reinterpret_cast<float *>(x.q + n + need);
-    s.data = need ? x.q + n : nullptr;
-    s.bytes = need;
-  } else {
-    x = i8_rows(a[5], a[6], r, device);
-    s = space_of(a[8], need, device);
+  Tensor Y = i8_output(a[7], r.M, w.N, X.scalar_type(), device);
+  const bool scratch = !has(a[5]) && !has(a[6]) && !has(a[8]);
+  I8Rows x = i8_rows(a[5], a[6], r, device);
+  Space s = space_of(a[8], device);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(device);
+    if (!Y.defined()) Y = fresh({r.M, w.N}, X.scalar_type(), device);
+    const size_t need = entry.i8_workspace_bytes(r.M, w.N, r.K);
+    if (scratch) {
+      // scratch in one piece: the rows (16-byte multiples, or the library refuses K), the workspace, the scales
+      const size_t n = (static_cast<size_t>(r.M) * r.K + 15) / 16 * 16;
+      s.kept = fresh({static_cast<int64_t>(n + need + 4 * static_cast<size_t>(r.M))}, at::kChar, device);
+      x.q = static_cast<int8_t *>(s.kept.data_ptr());
+      x.s = reinterpret_cast<float *>(x.q + n + need);
+      s.data = need ? x.q + n : nullptr;
+      s.bytes = need;
+    } else {
+      x.make(r, device);
+      s.make(need, device);
+    }
+    st = entry.i8_linear_forward(X.data_ptr(), r.stride, code, r.M, col, w.wq, w.scale, w.bias, w.N, r.K, x.q, x.s, Y.data_ptr(),
+                                 s.data, s.bytes, stream_of(device));
   }
-  const svdq_status st = entry.i8_linear_forward(X.data_ptr(), r.stride, code, r.M, col, w.wq, w.scale, w.bias, w.N, r.K, x.q, x.s,
-                                                 Y.data_ptr(), s.data, s.bytes, stream_of(device));
   return st != SVDQ_OK ? status(st) : wrap(Y);
 }
 
@@ -405,22 +450,30 @@ PyObject *rope_axes_table(PyObject *const *a) {
   const int M = count(pos.size(0), "tokens");
   int64_t P = 0;
   for (int i = 0; i < ax->n_axes && i < 4; ++i) P += ax->pairs[i];
-  const c10::cuda::CUDAGuard guard(pos.device());
   Tensor table;
   if (has(a[2])) {
     values(a[2], "table", 2 * P * M, at::kFloat, pos.device());
     table = tensor(a[2], "table");
-  } else {
-    table = fresh({M, P, 2}, at::kFloat, pos.device());
   }
-  const svdq_status st = entry.rope_axes_table(&p, M, ax, static_cast<float *>(table.data_ptr()), stream_of(pos.device()));
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(pos.device());
+    if (!table.defined()) table = fresh({M, P, 2}, at::kFloat, pos.device());
+    st = entry.rope_axes_table(&p, M, ax, static_cast<float *>(table.data_ptr()), stream_of(pos.device()));
+  }
   return st != SVDQ_OK ? status(st) : wrap(table);
 }
 
-// Heads [M, H, D] and their output.
+// Heads [M, H, D] and their output: the caller's or a new one.
 struct Heads {
-  svdq_heads in, out;
+  svdq_heads in{}, out{};
   Tensor kept;
+
+  void make(const Tensor &t) {
+    if (!kept.defined()) kept = fresh(t.sizes(), t.scalar_type(), t.device());
+    out = {kept.data_ptr(), in.heads, static_cast<size_t>(kept.stride(0)), static_cast<size_t>(kept.stride(1))};
+  }
 };
 Heads heads_of(const Tensor &t, PyObject *o, const char *name, const Tensor &like) {
   if (t.dim() != 3 || t.scalar_type() != like.scalar_type() || t.device() != like.device() || t.size(0) != like.size(0) ||
@@ -432,13 +485,10 @@ Heads heads_of(const Tensor &t, PyObject *o, const char *name, const Tensor &lik
     if (u.dim() != 3 || u.sizes() != t.sizes() || u.scalar_type() != t.scalar_type() || u.device() != t.device())
       refuse(std::string(name) + "_out must be like " + name);
     h.kept = u;
-  } else {
-    h.kept = fresh(t.sizes(), t.scalar_type(), t.device());
   }
-  if (t.size(2) > 1 && (t.stride(2) != 1 || h.kept.stride(2) != 1)) refuse("the columns of " + std::string(name) + " and its output must be contiguous");
-  const int n = count(t.size(1), "heads");
-  h.in = {t.data_ptr(), n, static_cast<size_t>(t.stride(0)), static_cast<size_t>(t.stride(1))};
-  h.out = {h.kept.data_ptr(), n, static_cast<size_t>(h.kept.stride(0)), static_cast<size_t>(h.kept.stride(1))};
+  if (t.size(2) > 1 && (t.stride(2) != 1 || (has(o) && h.kept.stride(2) != 1)))
+    refuse("the columns of " + std::string(name) + " and its output must be contiguous");
+  h.in = {t.data_ptr(), count(t.size(1), "heads"), static_cast<size_t>(t.stride(0)), static_cast<size_t>(t.stride(1))};
   return h;
 }
 
@@ -451,14 +501,19 @@ PyObject *rope_axes_apply(PyObject *const *a) {
   const svdq_rope_axes *ax = axes_of(a[3]);
   const svdq_positions p = positions_of(pos, *ax);
   if (pos.size(0) != q.size(0) || pos.device() != q.device()) refuse("pos must have q's tokens and device");
-  const c10::cuda::CUDAGuard guard(q.device());
-  const Heads hq = heads_of(q, a[5], "q", q);
-  Heads hk;
-  const bool k = has(a[1]);
-  if (k) hk = heads_of(tensor(a[1], "k"), a[6], "k", q);
-  const svdq_status st = entry.rope_axes_apply(&hq.in, &hq.out, k ? &hk.in : nullptr, k ? &hk.out : nullptr, code,
-                                               count(q.size(0), "tokens"), count(q.size(2), "columns"), &p, ax, truth(a[4]) ? 1 : 0,
-                                               stream_of(q.device()));
+  const int M = count(q.size(0), "tokens"), D = count(q.size(2), "columns"), inverse = truth(a[4]) ? 1 : 0;
+  Heads hq = heads_of(q, a[5], "q", q), hk;
+  const Tensor *k = has(a[1]) ? &tensor(a[1], "k") : nullptr;
+  if (k) hk = heads_of(*k, a[6], "k", q);
+  svdq_status st;
+  {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(q.device());
+    hq.make(q);
+    if (k) hk.make(*k);
+    st = entry.rope_axes_apply(&hq.in, &hq.out, k ? &hk.in : nullptr, k ? &hk.out : nullptr, code, M, D, &p, ax, inverse,
+                               stream_of(q.device()));
+  }
   return st != SVDQ_OK ? status(st) : tuple({hq.kept, hk.kept});
 }
 

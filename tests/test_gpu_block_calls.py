@@ -165,3 +165,41 @@ def test_rows_far_from_zero(M, K, far, deviation):
     R.assert_within(rstd[:, None], rs, rel * rs)
     R.assert_within(mean[:, None], mu, off.amax(1, keepdim=True) + R.U * mu.abs())
     R.assert_within(Y, c * rs, rs * off * (1 + rel) + (rel + 4 * R.U) * (c * rs).abs())
+
+
+def test_other_threads_run_while_a_call_waits():
+    """A call that waits in the library (for memory, for a full launch queue) leaves the interpreter to the other
+    threads. In the place of the library's functions, a C function that sleeps as many microseconds as xq has rows."""
+    import ctypes
+    import threading
+    import time
+
+    svdq = _svdq()
+    native, lib, libc = svdq._native(), svdq.load(), ctypes.CDLL(None)
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    own = [address(getattr(lib, "svdq_" + name)) for name in svdq._BOUND]
+    fakes = dict(i8_workspace_bytes=address(libc.usleep), i8_gemm=address(lib.svdq_version))
+    xq = torch.zeros(400000, 16, dtype=torch.int8, device="cuda")
+    wq, xs, ws = xq[:16], torch.zeros(400000, device="cuda"), torch.zeros(16, device="cuda")
+    Y = torch.empty(400000, 16, dtype=BF16, device="cuda")
+    turns, stop = [], threading.Event()
+
+    def count():
+        while not stop.is_set():
+            turns.append(time.perf_counter())
+            time.sleep(0.002)
+
+    other = threading.Thread(target=count)
+    try:
+        native.bind(*(fakes.get(name, at) for name, at in zip(svdq._BOUND, own)))
+        other.start()
+        start = time.perf_counter()
+        got = native.i8_gemm(xq, xs, wq, ws, None, Y, 0, None)
+        end = time.perf_counter()
+    finally:
+        native.bind(*own)
+        stop.set()
+        other.join()
+    assert isinstance(got, int) and got == lib.svdq_version()  # (what the fake returned as a status)
+    assert end - start >= 0.4
+    assert sum(start + 0.05 < t < end - 0.05 for t in turns) >= 10
