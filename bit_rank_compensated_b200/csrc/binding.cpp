@@ -126,7 +126,11 @@ float number(PyObject *o) {
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
   return static_cast<float>(v);
 }
-bool truth(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
 
 // While a call allocates and launches, other threads may run Python: an allocation can be slow, and a launch can wait for a
 // full queue, whose next entry may be a host function that needs the interpreter. Nothing in its scope touches a

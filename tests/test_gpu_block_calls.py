@@ -203,3 +203,14 @@ def test_other_threads_run_while_a_call_waits():
     assert isinstance(got, int) and got == lib.svdq_version()  # (what the fake returned as a status)
     assert end - start >= 0.4
     assert sum(start + 0.05 < t < end - 0.05 for t in turns) >= 10
+
+
+def test_a_flag_without_a_truth_value_is_an_error():
+    svdq = _svdq()
+    X, st = _normal(4, 64, seed=40), torch.zeros(4, device="cuda")
+    flag = torch.ones(2)  # "Boolean value of Tensor with more than one value is ambiguous"
+    q, pos = X.unflatten(1, (2, 32)), torch.zeros(4, 1, dtype=torch.int64, device="cuda")
+    for f in (lambda: svdq.layer_norm(X, stats=flag), lambda: svdq.layer_norm_backward(X, X, st, st, need_dX=flag),
+              lambda: svdq.rope_axes_apply(q, None, pos, svdq.RopeAxes((16,)), inverse=flag)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            f()
