@@ -8,7 +8,7 @@ The eigen-solver library used by the offline prepare step is loaded at run time;
 the copy bundled with the installed nvidia-cusolver wheel is baked in as a hint.
 
 csrc/binding.cpp (the Python calls of the operators around the projections) is compiled against the
-installed torch into bit_rank_compensated_b200/_binding.so.
+installed torch into bit_rank_compensated_b200/_binding.so; without torch only the library is built.
 """
 from __future__ import annotations
 
@@ -56,28 +56,43 @@ def _newest_header() -> float:
     return max(os.path.getmtime(h) for h in hs)
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """Compiles csrc/binding.cpp against the installed torch."""
-    src = os.path.join(CSRC, "binding.cpp")
-    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "svdq.h")), os.path.getmtime(__file__))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+def _binding_command(torch) -> list[str]:
     import sysconfig
 
-    import torch
-
-    base = os.path.join(os.path.dirname(torch.__file__))
+    src = os.path.join(CSRC, "binding.cpp")
+    base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
-    includes = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+    includes = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     lib = os.path.join(base, "lib")
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes[1:]],
-           f"-I{INCLUDE}", src, "-o", BINDING, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-           f"-Wl,-rpath,{lib}"]
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes],
+            f"-I{INCLUDE}", src, "-o", BINDING, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            f"-Wl,-rpath,{lib}"]
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str | None:
+    """Compiles csrc/binding.cpp against the installed torch, again where it or torch or Python has changed since.
+    Without torch there is nothing to bind: None."""
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: libsvdq.so is built, the Python binding is not", file=sys.stderr)
+        return None
+    cmd = _binding_command(torch)
+    made_for = "\n".join([torch.__version__, sys.version, *cmd])
+    record = os.path.join(BUILD, "binding.txt")
+    newest = max(os.path.getmtime(f) for f in (os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "svdq.h"), __file__))
+    if not force and os.path.exists(BINDING) and os.path.exists(record) and os.path.getmtime(BINDING) >= newest:
+        with open(record) as f:
+            if f.read() == made_for:
+                return BINDING
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(record, "w") as f:
+        f.write(made_for)
     return BINDING
 
 
