@@ -536,6 +536,8 @@ def _native():
 
 def _on_stream(stream, fn, *args):
     """Runs fn with `stream` as the current one, so that what it allocates belongs to that stream."""
+    if isinstance(args[0], torch.Tensor) and args[0].device != stream.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {args[0].device}")
     with torch.cuda.stream(stream):
         return fn(*args)
 
