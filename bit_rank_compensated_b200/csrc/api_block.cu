@@ -243,8 +243,8 @@ svdq_status svdq_i8_linear_forward(const void *X, size_t x_stride, int dtype, in
                                    float *x_scale, void *Y, void *workspace, size_t workspace_bytes, void *stream) {
   svdq_status st = check_gemm(xq, x_scale, M, wq, w_scale, bias, N, K, Y, dtype, workspace, workspace_bytes);
   if (st != SVDQ_OK) return st;
-  if (M > 0 && i8_few_fits(M, K)) {
-    // few tokens: quantized where they are multiplied, in one launch
+  if (M > 0 && i8_few_fits(M, N, K)) {
+    // few tokens and short rows: quantized where they are multiplied, in one launch
     if ((st = check_quantize(X, x_stride, dtype, M, K, col_scale, xq, x_scale)) != SVDQ_OK) return st;
     DeviceState *d = nullptr;
     if ((st = device_check(&d)) != SVDQ_OK) return st;

@@ -68,9 +68,9 @@ struct I8GemmLaunch {
   cudaStream_t stream;
 };
 cudaError_t launch_i8_gemm(const I8GemmLaunch &a);
-// The same of up to kFewTokens tokens, from int8 rows or (where their alignment allows) floating ones.
-constexpr int kFewTokens = 8;
-bool i8_few_fits(int M, int K);
+// The same of up to eight tokens, from int8 rows or floating ones: whether they are few, and whether their rows are
+// quantized where they are multiplied.
+bool i8_few_fits(int M, int N, int K);
 bool i8_few_quantizes(const QuantRowsLaunch &q);
 cudaError_t launch_i8_few(const I8GemmLaunch &a);
 cudaError_t launch_i8_few_quantized(const QuantRowsLaunch &q, const I8GemmLaunch &a);

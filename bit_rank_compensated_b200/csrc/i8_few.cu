@@ -4,9 +4,8 @@
 //
 // A tensor-core tile would be nearly empty and its pipeline costs more than the product (19 us for 4096 x
 // 4096 and one token), so the CUDA cores multiply: four int8 products an instruction (dp4a). The tokens'
-// codes lie in shared memory; where the caller has floating rows, every block quantizes them itself
-// (the row quantizer's own arithmetic: the same codes), which costs it one more read of M rows from
-// L2 and saves a launch.
+// codes lie in shared memory; where the caller has floating rows and they are short, every block quantizes
+// them itself (the row quantizer's own arithmetic: the same codes), which saves a launch.
 //
 // A block of eight warps takes CB channels for each WN-th of its warps and shares the K axis out among
 // the WK = 8 / WN others: a lane multiplies 16 bytes of each channel's row with the same bytes of every
@@ -24,6 +23,8 @@ constexpr int kWarps = 8;
 constexpr int CB = 4;        // channels of a warp
 constexpr int CHUNK = 512;   // bytes of a row that a warp reads at once
 constexpr int kMaxCodes = 96 * 1024;  // bytes of shared memory for the tokens' codes
+constexpr int kMaxQuantized = 8192;   // codes that a block makes itself (i8_few_quantizes)
+constexpr int kWideChannels = 37 * 256, kShortRow = 1536;  // i8_few_fits
 
 struct FewArgs {
   // floating rows and their smoothing, or int8 rows and their scales
@@ -199,7 +200,7 @@ cudaError_t launch_mt(FewArgs a, int num_sms, cudaStream_t st) {
   const int rounds = (a.tasks + resident * num_sms - 1) / (resident * num_sms);
   const dim3 grid((a.tasks + rounds - 1) / rounds);
   auto kern = k_i8_few<T, MT, QUANT>;
-  const cudaError_t e = allow_smem<kMaxCodes>(kern);
+  const cudaError_t e = allow_smem<QUANT ? kMaxQuantized : kMaxCodes>(kern);
   return e != cudaSuccess ? e : launch_dependent(kern, grid, 32 * kWarps, smem, st, a);
 }
 
@@ -222,9 +223,21 @@ int padded_tokens(int M) { return M <= 2 ? M : (M <= 4 ? 4 : 8); }
 
 }  // namespace
 
-bool i8_few_fits(int M, int K) { return M <= kFewTokens && static_cast<int64_t>(padded_tokens(M)) * K <= kMaxCodes; }
+// Against the tensor cores, from int8 rows (us): 4096 x 4096 5.5 and 10.7 for one token, 7.5 and 10.7 for four, 9.7 and
+// 10.7 for eight; 12288 x 4096 (N x K) 11.7 and 22.3, 14.7 and 19.3, 22.2 and 18.9. Five tokens and more multiply as
+// eight and are bound by that: where the tensor cores' tiles are enough without a split of the K axis and it is not
+// short (12288 x 1536: 9.9 and 9.5), they are left to them.
+bool i8_few_fits(int M, int N, int K) {
+  if (M > 8 || static_cast<int64_t>(padded_tokens(M)) * K > kMaxCodes) return false;
+  return M <= 4 || N <= kWideChannels || K <= kShortRow;
+}
 
+// Each of several hundred blocks quantizes the rows for itself, which saves a launch (2 us of the host) but costs by
+// what there is to quantize. In the block and by the row quantizer (us, bf16): one token, 4096 x 4096 7.4 and 6.6;
+// two tokens 8.8 and 7.4; four, 4096 x 2048 7.8 and 6.4; eight, 4096 x 1024 6.3 and 5.2; and beyond, four tokens,
+// 4096 x 4096 12.3 and 8.8; eight 17.9 and 11.0.
 bool i8_few_quantizes(const QuantRowsLaunch &q) {
+  if (padded_tokens(q.M) * q.K > kMaxQuantized) return false;
   const size_t e = q.dtype == SVDQ_F32 ? 4 : 2;
   return rows_aligned(q.X, q.M > 1 ? q.x_stride : 0, e, 16) && rows_aligned(q.col_scale, 0, 4, 16);
 }

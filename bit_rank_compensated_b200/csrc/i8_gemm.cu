@@ -394,13 +394,13 @@ cudaError_t launch_t(const I8GemmLaunch &g) {
 }  // namespace
 
 size_t i8_gemm_workspace_bytes(int M, int N, int K) {
-  if (i8_few_fits(M, K)) return 0;
+  if (i8_few_fits(M, N, K)) return 0;
   const int s = splits_of(M, N, K, kPairs);
   return s > 1 ? 4 * static_cast<size_t>(s) * M * N : 0;
 }
 
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g) {
-  if (i8_few_fits(g.M, g.K)) return launch_i8_few(g);
+  if (i8_few_fits(g.M, g.N, g.K)) return launch_i8_few(g);
   if (static_cast<int64_t>((g.M + 2 * BM - 1) / (2 * BM)) * ((g.N + BN - 1) / BN) >= (1ll << 30)) return cudaErrorInvalidValue;
   if (g.y_dtype == SVDQ_F32) return launch_t<float>(g);
   if (g.y_dtype == SVDQ_F16) return launch_t<__half>(g);

@@ -214,3 +214,25 @@ def test_a_flag_without_a_truth_value_is_an_error():
               lambda: svdq.rope_axes_apply(q, None, pos, svdq.RopeAxes((16,)), inverse=flag)):
         with pytest.raises(RuntimeError, match="ambiguous"):
             f()
+
+
+# ---------------------------------------------------------------- few tokens
+@pytest.mark.parametrize("N,K", [(272, 1024), (272, 1040), (272, 2048), (272, 4112), (64, 8208), (9472, 1552), (9488, 1536),
+                                 (9488, 1552)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_tokens_by_every_way(N, K, dtype):
+    """Rows quantized where they are multiplied, rows quantized before, tokens left to the tensor cores: the sums are
+    exact and the codes the same, so a token's output does not depend on the way."""
+    svdq = _svdq()
+    X = _normal(9, K, seed=50, dtype=dtype)
+    col = _normal(K, seed=51).abs() + 0.5
+    wq, ws = svdq.i8_quantize_rows(_normal(N, K, seed=52, dtype=BF16))
+    b = _normal(N, seed=53)
+    every = svdq.i8_linear_forward(X, wq, ws, b, col_scale=col)
+    q, s = R.quantize_rows(X, col)
+    y, err = R.i8_product(q, s, wq, ws, b)
+    R.assert_within(every, y, R.allowed(y, dtype, err))
+    for M in range(1, 9):
+        assert torch.equal(svdq.i8_linear_forward(X[:M], wq, ws, b, col_scale=col), every[:M])
+        assert torch.equal(svdq.i8_gemm(q[:M], s[:M], wq, ws, b, dtype=dtype), every[:M])
+    assert svdq.last_device_error() == 0
