@@ -12,6 +12,9 @@
 
 namespace svdq {
 
+// Pieces of `each` that make up n >= 1 (n + each may pass 31 bits).
+constexpr int pieces(int n, int each) { return (n - 1) / each + 1; }
+
 // Rows of X and the weight and bias their layer norm takes.
 struct NormLaunch {
   const void *X;

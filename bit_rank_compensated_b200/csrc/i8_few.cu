@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(32 * kWarps, MT <= 2 ? 4 : (MT == 4 ? 3 : 2)) 
   int task = blockIdx.x, chunk = wk;
   uint4 w[CB];
   auto fetch = [&](int t, int c) {
-    const int n0 = t * per_task + wn * CB, k = c * CHUNK + lane * 16;
+    const bool there = t < a.tasks;  // (behind the last task the channel may pass 31 bits)
+    const int n0 = there ? t * per_task + wn * CB : 0, k = c * CHUNK + lane * 16;
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
       w[i] = make_uint4(0, 0, 0, 0);
-      if (t < a.tasks && n0 + i < a.N && k < a.K) w[i] = ldg_stream(a.wq + static_cast<size_t>(n0 + i) * a.K + k);
+      if (there && n0 + i < a.N && k < a.K) w[i] = ldg_stream(a.wq + static_cast<size_t>(n0 + i) * a.K + k);
     }
   };
   fetch(task, chunk);
@@ -192,7 +193,7 @@ cudaError_t launch_mt(FewArgs a, int num_sms, cudaStream_t st) {
   a.chunks = (a.K + CHUNK - 1) / CHUNK;
   a.wk = a.chunks >= 8 ? 8 : (a.chunks >= 4 ? 4 : (a.chunks >= 2 ? 2 : 1));
   const int per_task = CB * (kWarps / a.wk);
-  a.tasks = (a.N + per_task - 1) / per_task;
+  a.tasks = pieces(a.N, per_task);
   const int smem = MT * a.K;
   // blocks that an SM holds at once, by registers and by the codes' share of its memory
   int resident = MT <= 2 ? 4 : (MT == 4 ? 3 : 2);

@@ -341,7 +341,7 @@ int steps_of(int K) { return (K + STEP - 1) / STEP; }
 // about 5 TB/s): split into the number of shares for which the sum is least,
 // of four steps at least and no more than there are pairs to take them.
 int splits_of(int M, int N, int K, int pairs) {
-  const int64_t tiles = static_cast<int64_t>((M + 2 * BM - 1) / (2 * BM)) * ((N + BN - 1) / BN);
+  const int64_t tiles = static_cast<int64_t>(pieces(M, 2 * BM)) * pieces(N, BN);
   const int steps = steps_of(K);
   if (2 * tiles > pairs) return 1;
   int most = static_cast<int>(pairs / tiles);
@@ -377,7 +377,7 @@ cudaError_t launch_t(const I8GemmLaunch &g) {
   const bool mapped = splits > 1 ? make_map_3d(&ty, CU_TENSOR_MAP_DATA_TYPE_INT32, g.workspace, g.N, g.M, splits, 4, 32, BM, CU_TENSOR_MAP_SWIZZLE_128B)
                                  : make_map(&ty, dt, g.Y, g.N, g.M, g.N * e, 128 / e, BM, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!mapped) return cudaErrorInvalidValue;
-  const GArgs a{g.x_scale, g.w_scale, g.bias, g.M, g.N, g.K, (g.M + 2 * BM - 1) / (2 * BM), (g.N + BN - 1) / BN, splits, each, g.dev->err};
+  const GArgs a{g.x_scale, g.w_scale, g.bias, g.M, g.N, g.K, pieces(g.M, 2 * BM), pieces(g.N, BN), splits, each, g.dev->err};
   auto kern = splits > 1 ? k_i8_gemm<int> : k_i8_gemm<T>;
   cudaError_t err = allow_smem<SMEM>(kern);
   if (err != cudaSuccess) return err;
@@ -401,7 +401,7 @@ size_t i8_gemm_workspace_bytes(int M, int N, int K) {
 
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g) {
   if (i8_few_fits(g.M, g.N, g.K)) return launch_i8_few(g);
-  if (static_cast<int64_t>((g.M + 2 * BM - 1) / (2 * BM)) * ((g.N + BN - 1) / BN) >= (1ll << 30)) return cudaErrorInvalidValue;
+  if (static_cast<int64_t>(pieces(g.M, 2 * BM)) * pieces(g.N, BN) >= (1ll << 30)) return cudaErrorInvalidValue;
   if (g.y_dtype == SVDQ_F32) return launch_t<float>(g);
   if (g.y_dtype == SVDQ_F16) return launch_t<__half>(g);
   return launch_t<__nv_bfloat16>(g);

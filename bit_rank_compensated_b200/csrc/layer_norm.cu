@@ -286,7 +286,7 @@ struct Slices {
   int slices, chunk;
 };
 Slices slices_of(int M, int K, int rows_per_group, int least) {
-  const int used = (M - 1) / rows_per_group + 1;  // (M + rows_per_group may pass 32 bits)
+  const int used = pieces(M, rows_per_group);
   const int rows = M < rows_per_group ? M : rows_per_group;
   const int threads = for_row(K, [K]<int TEAM, int E>() { return row_threads(K, E); });
   int s = 148 * blocks_per_sm(threads, kBackwardThreads) / used;

@@ -236,3 +236,30 @@ def test_few_tokens_by_every_way(N, K, dtype):
         assert torch.equal(svdq.i8_linear_forward(X[:M], wq, ws, b, col_scale=col), every[:M])
         assert torch.equal(svdq.i8_gemm(q[:M], s[:M], wq, ws, b, dtype=dtype), every[:M])
     assert svdq.last_device_error() == 0
+
+
+@pytest.mark.parametrize("M", [1, 8, 9])
+def test_as_many_channels_as_an_int_counts(M):
+    """N = 2^31 - 16: a tile's or task's size added to it passes 31 bits. Weight rows of zeros but at the ends."""
+    svdq = _svdq()
+    N, K, ends = 2 ** 31 - 16, 16, 400
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("about 90 GB of device memory")
+    try:
+        xq = torch.randint(-127, 128, (M, K), generator=torch.Generator("cuda").manual_seed(60), device="cuda", dtype=torch.int8)
+        wq = torch.zeros(N, K, dtype=torch.int8, device="cuda")
+        for part in (wq[:ends], wq[-ends:]):
+            part.copy_(torch.randint(-127, 128, (ends, K), generator=torch.Generator("cuda").manual_seed(61), device="cuda"))
+        xs, ws = torch.rand(M, device="cuda") + 0.5, torch.ones(N, device="cuda")
+        Y = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+        svdq.i8_gemm(xq, xs, wq, ws, Y=Y)
+        for at in (slice(0, ends), slice(N - ends, N)):
+            y, err = R.i8_product(xq, xs, wq[at], ws[at], None)
+            R.assert_within(Y[:, at], y, R.allowed(y, BF16, err))
+        for m in range(M):
+            for part in Y[m, ends:N - ends].split(2 ** 29):
+                assert int(torch.count_nonzero(part)) == 0
+    finally:
+        xq = wq = xs = ws = Y = part = None
+        torch.cuda.empty_cache()
+    assert svdq.last_device_error() == 0
