@@ -63,16 +63,6 @@ struct GArgs {
   uint32_t *err;
 };
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // A value from its sum: scaled in fp32, one fp32 rounding each for the sum, the two scales and the bias.
 __device__ __forceinline__ float scaled(int acc, float xs, float ws, float b) {
   return fmaf(__fmul_rn(static_cast<float>(acc), xs), ws, b);
@@ -259,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                   w[half][i][j][0] = __float_as_uint(v0);
                   w[half][i][j][1] = __float_as_uint(v1);
                 } else {
-                  w[half][i][j][0] = pack2<T>(v0, v1);
+                  w[half][i][j][0] = narrow(pair(v0, v1), T{});
                 }
               }
             }
@@ -331,7 +321,7 @@ __global__ void __launch_bounds__(256) k_i8_shares(const int *part, GArgs a, T *
     for (int e = 0; e < 4; ++e) b[e] = a.bias[n + e];
   const float v[4] = {scaled(s.x, xs, ws[0], b[0]), scaled(s.y, xs, ws[1], b[1]), scaled(s.z, xs, ws[2], b[2]), scaled(s.w, xs, ws[3], b[3])};
   if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(Y + i) = make_float4(v[0], v[1], v[2], v[3]);
-  else *reinterpret_cast<uint2 *>(Y + i) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  else *reinterpret_cast<uint2 *>(Y + i) = make_uint2(narrow(pair(v[0], v[1]), T{}), narrow(pair(v[2], v[3]), T{}));
 }
 
 int steps_of(int K) { return (K + STEP - 1) / STEP; }

@@ -63,7 +63,6 @@ __global__ void __launch_bounds__(kThreads) k_rope_table(RopeLaunch a, int token
     __stcs(reinterpret_cast<float2 *>(a.table) + m * a.n_pairs + p, ladder(a.pos, m, p));
 }
 
-template <typename T>
 __device__ __forceinline__ void turn(float &u0, float &u1, float2 cs) {
   const float v0 = fmaf(u0, cs.x, -__fmul_rn(u1, cs.y));
   u1 = fmaf(u1, cs.x, __fmul_rn(u0, cs.y));
@@ -177,12 +176,12 @@ __global__ void __launch_bounds__(kThreads) k_rope_apply(RopeLaunch a, int units
             if constexpr (HALVES || VEC == 1) {
               v1[e].get(y);
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) turn<T>(x[i], y[i], cs[i]);
+              for (int i = 0; i < VEC; ++i) turn(x[i], y[i], cs[i]);
               v1[e].set(y);
             } else {
 #pragma unroll
               for (int i = 0; i < TURN; ++i)
-                if (u * TURN + i < P) turn<T>(x[2 * i], x[2 * i + 1], cs[i]);  // a pair behind the rotated ones stays
+                if (u * TURN + i < P) turn(x[2 * i], x[2 * i + 1], cs[i]);  // a pair behind the rotated ones stays
             }
             v0[e].set(x);
           }

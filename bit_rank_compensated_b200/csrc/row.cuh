@@ -26,21 +26,6 @@ __device__ __forceinline__ int row_column(int i) {
   return ((i / VEC) * t + static_cast<int>(threadIdx.x)) * VEC + i % VEC;
 }
 
-// Two 16-bit values of a word as fp32, and back.
-__device__ __forceinline__ f32x2 widen(uint32_t w, __nv_bfloat16) { return pair_bits(w << 16, w & 0xffff0000u); }
-__device__ __forceinline__ f32x2 widen(uint32_t w, __half) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-  return pair(f.x, f.y);
-}
-__device__ __forceinline__ uint32_t narrow(f32x2 v, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo(v), hi(v));
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t narrow(f32x2 v, __half) {
-  const __half2 h = __floats2half2_rn(lo(v), hi(v));
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <typename T, int TEAM, int VEC, int E, bool FULL>
 __device__ __forceinline__ void store_row(T *p, int K, const f32x2 (&y)[E / 2]) {
   if constexpr (VEC == 1) {
