@@ -50,6 +50,8 @@ const Tensor &tensor(PyObject *o, const char *name) {
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
   const Tensor &t = THPVariable_Unpack(o);
   if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+  // (of a conjugated tensor's imaginary part: its memory holds the other sign)
+  if (t.is_neg()) refuse(std::string(name) + " must not be a lazily negated view (resolve_neg() makes a plain tensor of it)");
   return t;
 }
 

@@ -263,3 +263,24 @@ def test_as_many_channels_as_an_int_counts(M):
         xq = wq = xs = ws = Y = part = None
         torch.cuda.empty_cache()
     assert svdq.last_device_error() == 0
+
+
+def test_lazily_negated_views_are_refused():
+    """The imaginary part of a conjugated tensor is a view whose memory holds the other sign."""
+    svdq = _svdq()
+    z = torch.complex(_normal(4, 64, seed=70), _normal(4, 64, seed=71))
+    assert z.conj().imag.is_neg()
+    rows = z.imag.contiguous()
+    negated = torch._neg_view(rows)
+    assert negated.is_neg() and torch.equal(negated, -rows)
+    q, pos, axes = negated.unflatten(1, (2, 32)), torch.zeros(4, 1, dtype=torch.int64, device="cuda"), svdq.RopeAxes((16,))
+    one, w = torch.ones(4, device="cuda"), torch._neg_view(torch.ones(64, device="cuda"))
+    for f in (lambda: svdq.layer_norm(negated), lambda: svdq.layer_norm(rows, w), lambda: svdq.layer_norm(rows, None, w),
+              lambda: svdq.layer_norm(rows, Y=negated), lambda: svdq.layer_norm_backward(negated, rows, one, one),
+              lambda: svdq.layer_norm_backward(rows, negated, one, one), lambda: svdq.i8_quantize_rows(negated),
+              lambda: svdq.i8_quantize_rows(rows, w), lambda: svdq.i8_layer_norm_quantize(negated),
+              lambda: svdq.rope_axes_apply(q, None, pos, axes), lambda: svdq.rope_axes_apply(q.resolve_neg(), q, pos, axes),
+              lambda: svdq.rope_axes_table(torch._neg_view(pos.float()), axes)):
+        with pytest.raises(ValueError, match="resolve_neg"):
+            f()
+    assert torch.equal(svdq.layer_norm(negated.resolve_neg()), -svdq.layer_norm(rows))
