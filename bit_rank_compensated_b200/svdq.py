@@ -511,7 +511,10 @@ def unfused_forward(X, layer, bufs, Y, stream=None):
 # ---------------------------------------------------------------- operators around the projections
 # These check what they are given (shapes, types, strides, devices; ValueError), since their rows may be
 # strided views, and run on the tensors' device whichever is current. csrc/binding.cpp does that and calls
-# the library: a small call's time is its caller's.
+# the library: a small call's time is its caller's. They are not recorded by autograd: what they return is
+# detached, and what they write in place is not counted as changed, whatever their inputs require. A gradient is a
+# call of its own (layer_norm_backward; rope_axes_apply with inverse), for the backward of the caller's
+# torch.autograd.Function; the linears here have none.
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3, torch.int64: 4}
 _BOUND = ("layer_norm", "layer_norm_workspace_bytes", "layer_norm_backward", "i8_quantize_rows",
           "i8_layer_norm_quantize", "i8_workspace_bytes", "i8_gemm", "i8_linear_forward", "rope_axes_table",
@@ -548,7 +551,8 @@ def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset
 
     weight, bias: [K], or [groups, K] where row m takes group m // rows_per_group (0: the rows shared out
     evenly), e.g. the scale and shift of a modulation with weight_offset 1; views of one projection's
-    output will do. Y may be X. With stats also returns mean and rstd (fp32 [M]) for the backward pass."""
+    output will do. Y may be X. With stats also returns mean and rstd (fp32 [M]) for the backward pass. The result is
+    detached from autograd."""
     if stream is not None:
         return _on_stream(stream, layer_norm, X, weight, bias, rows_per_group, weight_offset, eps, Y, stats)
     r = (_binding or _native()).layer_norm(X, weight, bias, rows_per_group, weight_offset, eps, Y, stats)
@@ -560,8 +564,8 @@ def layer_norm(X, weight=None, bias=None, rows_per_group: int = 0, weight_offset
 def layer_norm_backward(dY, X, mean, rstd, weight=None, rows_per_group: int = 0, weight_offset: float = 0.0, dX=None,
                         groups: int | None = None, need_dX: bool = True, need_dweight: bool = True,
                         need_dbias: bool = True, workspace=None, stream=None):
-    """(dX, dweight, dbias) of layer_norm for the output's gradient dY; dX of X's type, dweight and dbias
-    fp32 [groups, K]. None in the place of what is not needed. dX may be dY or X. Without a weight,
+    """(dX, dweight, dbias) of layer_norm for the output's gradient dY, which the caller has (from autograd, say, in
+    the backward of its torch.autograd.Function around layer_norm); dX of X's type, dweight and dbias fp32 [groups, K]. None in the place of what is not needed. dX may be dY or X. Without a weight,
     groups gives the number of the bias's groups."""
     if stream is not None:
         return _on_stream(stream, layer_norm_backward, dY, X, mean, rstd, weight, rows_per_group, weight_offset, dX,
@@ -657,7 +661,7 @@ def rope_axes_table(pos, axes: RopeAxes, table=None, stream=None):
 
 def rope_axes_apply(q, k, pos, axes: RopeAxes, inverse: bool = False, q_out=None, k_out=None, stream=None):
     """Rotates the heads q [M, Hq, D] and k [M, Hk, D] (or None) by the positions pos [M, axes], with no table;
-    with inverse, back: the gradient of the rotation. Views of a packed projection will do; q_out and k_out may
+    with inverse, back: the gradient of the rotation (the results are detached from autograd). Views of a packed projection will do; q_out and k_out may
     be q and k. Returns (q_out, k_out)."""
     if stream is not None:
         return _on_stream(stream, rope_axes_apply, q, k, pos, axes, inverse, q_out, k_out)

@@ -314,7 +314,8 @@ typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_F16 = 1, SVDQ_F32 = 2, SVDQ_I32 = 
 
 /* Weight and bias of a layer norm, one row of K values for each group of consecutive rows of X
  * (a batch's samples, each under its own shift and scale, or one group for a plain weight).
- * Row m of X takes row m / rows_per_group; groups * rows_per_group >= M. */
+ * Row m of X takes row m / rows_per_group; groups * rows_per_group >= M. From M on, rows_per_group makes one group
+ * of all rows. */
 typedef struct svdq_norm_affine {
   const void *weight; /* groups rows of K, or NULL: factor 1 */
   const void *bias;   /* groups rows of K, or NULL: 0 */
@@ -327,6 +328,7 @@ typedef struct svdq_norm_affine {
 
 /* Layer norm over the K columns of every row, with statistics in fp32:
  *   xhat = (x - mean) * rstd,  mean = sum(x) / K,  rstd = 1 / sqrt(sum((x - mean)^2) / K + eps)
+ *   (a row of one value has xhat 0)
  *   Y    = xhat * (weight_offset + weight) + bias
  *   X, Y    device, M x K of dtype (Y may be X).
  *   affine  host struct, or NULL for Y = xhat.
@@ -374,8 +376,8 @@ SVDQ_API svdq_status svdq_layer_norm_backward(const void *dY, size_t dy_stride, 
  *     workspace  device, 16-byte aligned, at least svdq_i8_workspace_bytes(M, N, K) bytes (may be 0,
  *                then NULL is fine): partial sums where few tokens leave the K axis to be split.
  * svdq_i8_linear_forward: svdq_i8_quantize_rows, then svdq_i8_gemm with Y of X's dtype: the same bits.
- *     xq and x_scale are scratch of the sizes above, with no defined contents afterwards (few tokens
- *     are quantized where they are multiplied).
+ *     xq and x_scale are scratch of the sizes above, with no defined contents afterwards (a few short
+ *     rows are quantized where they are multiplied).
  * Asynchronous on stream. */
 SVDQ_API svdq_status svdq_i8_quantize_rows(const void *X, size_t x_stride, int dtype, int M, int K,
                                            const float *col_scale, int8_t *xq, float *x_scale, void *stream);

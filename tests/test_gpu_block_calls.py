@@ -284,3 +284,70 @@ def test_lazily_negated_views_are_refused():
         with pytest.raises(ValueError, match="resolve_neg"):
             f()
     assert torch.equal(svdq.layer_norm(negated.resolve_neg()), -svdq.layer_norm(rows))
+
+
+# ---------------------------------------------------------------- autograd
+def test_calls_are_detached():
+    svdq = _svdq()
+    X = _normal(4, 64, seed=80).requires_grad_()
+    w = _normal(64, seed=81).requires_grad_()
+    q = X.unflatten(1, (2, 32))
+    pos, axes = torch.zeros(4, 1, dtype=torch.int64, device="cuda"), svdq.RopeAxes((16,))
+    wq, ws = svdq.i8_quantize_rows(_normal(16, 64, seed=82))
+    for y in (svdq.layer_norm(X, w), svdq.rope_axes_apply(q, None, pos, axes)[0], svdq.i8_linear_forward(X, wq, ws)):
+        assert not y.requires_grad
+
+
+@pytest.mark.parametrize("M,groups", [(1, 1), (37, 3), (600, 2)])
+def test_gradients_in_a_function_of_the_callers(M, groups):
+    """Norm and rotation as one torch.autograd.Function, as the tuning of a block's norms makes it: the gradients of
+    fp32 leaves against those of the formula under autograd in 64 bits, by the bounds of each call."""
+    svdq = _svdq()
+    K, heads, rows = 256, 2, -(-M // groups)
+    pos, axes = torch.arange(M, device="cuda")[:, None] * 3, svdq.RopeAxes((32, 32))
+    pos = torch.cat([pos, pos // 5], 1)
+
+    class NormRotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, w, b):
+            Y, mean, rstd = svdq.layer_norm(X, w, b, rows_per_group=rows, weight_offset=1.0, stats=True)
+            ctx.save_for_backward(X, w, mean, rstd)
+            return svdq.rope_axes_apply(Y.unflatten(1, (heads, K // heads)), None, pos, axes)[0]
+
+        @staticmethod
+        def backward(ctx, dq):
+            X, w, mean, rstd = ctx.saved_tensors
+            dY = svdq.rope_axes_apply(dq.contiguous(), None, pos, axes, inverse=True)[0].flatten(1)
+            return svdq.layer_norm_backward(dY, X, mean, rstd, w, rows_per_group=rows, weight_offset=1.0)
+
+    leaves = [_normal(M, K, seed=90), _normal(groups, K, seed=91, scale=0.3), _normal(groups, K, seed=92, scale=0.3)]
+    dq = _normal(M, heads, K // heads, seed=93)
+    own = [t.clone().requires_grad_() for t in leaves]
+    got = torch.autograd.grad(NormRotate.apply(*own), own, dq)
+    x, w, b = [t.double().requires_grad_() for t in leaves]
+    d = x - x.mean(1, keepdim=True)
+    xhat = d / torch.sqrt((d * d).mean(1, keepdim=True) + R.EPS)
+    row = torch.arange(M, device="cuda") // rows
+    y = (xhat * (1 + w[row]) + b[row]).unflatten(1, (heads, K // heads))
+    cos, sin, angle = R.cos_sin(pos, (32, 32), 10000.0, False)
+    u, v = y[..., 0:128:2], y[..., 1:128:2]
+    turned = torch.stack([u * cos[:, None] - v * sin[:, None], v * cos[:, None] + u * sin[:, None]], -1).flatten(-2)
+    want = torch.autograd.grad(turned, (x, w, b), dq.double())
+    # the rotation back is within e |u| + |v| of each pair, and goes linearly through the norm's gradient; the
+    # statistics are within 140 U of theirs, which the gradient takes with a factor of its own size
+    e = 2.0 ** -22 + 2.0 ** -50 * float(angle.abs().max()) + 3 * R.U
+    dy, _ = R.rope(dq, cos, sin, angle, False, True)
+    dy = dy.flatten(1)
+    off = e * dq.double().abs().unflatten(-1, (-1, 2)).sum(-1).repeat_interleave(2, -1).flatten(1)
+    with torch.no_grad():
+        mean, rstd = x.mean(1), 1 / torch.sqrt((d * d).mean(1) + R.EPS)
+        _, bounds = R.layer_norm_backward(dy, leaves[0], mean, rstd, leaves[1], rows, groups, 1.0)
+        wa, r, xa = 1 + w.abs()[row], rstd[:, None], xhat.abs()
+        g, gdy = off * wa, dy.abs() * wa
+        stat = 300 * R.U * (1 + (x.abs().mean(1, keepdim=True) * r))
+        more = r * (g + g.mean(1, keepdim=True) + xa * (g * xa).mean(1, keepdim=True))
+        more = more + stat * r * (gdy + gdy.mean(1, keepdim=True) + (1 + xa) * (gdy * (1 + xa)).mean(1, keepdim=True)) * 3
+        grouped = lambda t: torch.zeros(groups, K, dtype=torch.float64, device="cuda").index_add(0, row, t)  # noqa: E731
+        R.assert_within(got[0], want[0], R.allowed(want[0], F32, bounds[0] + more))
+        R.assert_within(got[1], want[1], bounds[1] + grouped(off * xa + stat * dy.abs() * (1 + xa)) + 1e-30)
+        R.assert_within(got[2], want[2], bounds[2] + grouped(off) + 1e-30)
