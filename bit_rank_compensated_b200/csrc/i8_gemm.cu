@@ -12,9 +12,10 @@
 // product needs no scale, so int8 runs with no scale traffic in the loop (the 4-bit GEMM's blocks).
 //
 // What was measured: a step takes 0.28 us (550 cycles, 512 of them the MMAs') while the chip is not
-// full, and narrower tiles do not take less (256, 192, 128 and 64 channels: 13.4, 12.9, 12.8 and 13.4 us
-// for 16 tokens, 4096 x 4096, where they have as many steps), so there is one tile. Four output
-// groups instead of two cost 1.5 us a launch and 3 % of the large product. The output stage takes 2850 cycles a
+// full. There is one tile: for 16 tokens, 4096 x 4096, narrower ones took as long (256, 192, 128 and 64 channels:
+// 13.4, 12.9, 12.8 and 13.4 us, with an earlier output stage), since the weights' way in bounds them there. Where
+// the last wave of tiles is nearly empty (2202 x 4608: 162 tiles on 74 pairs take three waves for 2.2) a narrower
+// one was not measured. Four output groups instead of two cost 1.5 us a launch and 3 % of the large product. The output stage takes 2850 cycles a
 // tile (4100 to 6200 with a row to a thread, which reads every scale; converting the sums by
 // integer arithmetic instead of the conversion instruction made it slower).
 // Where there are at most half as many tiles as pairs, the K axis is split: each pair writes the raw sums of

@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(TEAM, blocks_per_sm(TEAM, kBackwardThreads)) k
       mean_n = a.mean[m + 1];
       rstd_n = a.rstd[m + 1];
     }
+    // (not beside the row, where -mean * rstd may overflow: 1537 x 1153 of fp32 in 11.4 us, 10.0 without the test of
+    // every column that rows without vectors pay for it)
     within_row<TEAM, VEC, E, FULL>(a.K, x, [&](f32x2 p, int) { return mul2(add2(p, minus), r2); });
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
